@@ -114,7 +114,8 @@ def node_attr(nd: dict) -> list:
 
 EXPORTS = ["hf_fusion_create", "hf_fusion_plan", "hf_fusion_source", "hf_fusion_launch",
            "hf_fusion_launch_noalloc", "hf_fusion_destroy", "hf_last_error", "hf_abi_version",
-           "hf_linear_index"]
+           "hf_linear_index", "hf_operator_create", "hf_operator_plan", "hf_operator_launch",
+           "hf_operator_launch_noalloc", "hf_operator_destroy"]
 SCRATCH_BYTES = 16 << 20  # HF_SCRATCH_BYTES: the no-allocation launch's scratch memory per GPU
 
 
@@ -373,3 +374,7 @@ class Fusion:
             self.close()
         except Exception:
             pass
+
+
+from .operators import (Dropout, GatedFeedForward, GatedFeedForwardGrad, Matmul, MatmulGrad,  # noqa: E402
+                        Operator, RmsNorm, RmsNormGrad)

@@ -2,8 +2,8 @@
 
 The host library (planner, code generator, hiprtc driver, C ABI) is plain C++
 compiled with g++ against the HIP runtime and hiprtc; the one device array the
-library holds itself (the no-allocation launch's scratch memory) is compiled
-with hipcc for gfx950 and linked in.  The hand-written
+library holds itself (the no-allocation launch's scratch memory) and the
+operators' kernels are compiled with hipcc for gfx950 and linked in.  The hand-written
 device templates under csrc/kernels are embedded into it as text; every
 fusion's kernel is generated from them and compiled for gfx950 by hiprtc at
 hf_fusion_create time.
@@ -22,7 +22,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhlofusion.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 TEMPLATES = ["common", "loop", "transpose", "reduce_row", "reduce_col"]
-SOURCES = ["intake.cpp", "plan.cpp", "codegen.cpp", "hlofusion.cpp"]
+SOURCES = ["intake.cpp", "plan.cpp", "codegen.cpp", "hlofusion.cpp", "operators/operators.cpp"]
 
 
 def embed() -> str:
@@ -41,24 +41,28 @@ def embed() -> str:
 
 
 # Device code compiled into the library itself (the no-allocation launch's
-# scratch array); compiled with hipcc for gfx950, without packed FP32.
-HIP_SOURCES = ["scratch.hip"]
-HIPCC_FLAGS = ["--offload-arch=gfx950", "-O2", "-std=c++17", "-fPIC",
+# scratch array, the operators' kernels); compiled with hipcc for gfx950,
+# without packed FP32, one process a file.
+HIP_SOURCES = ["scratch.hip", "operators/rows.hip", "operators/product.hip", "operators/skinny.hip"]
+HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 
 def build(verbose: bool = False) -> str:
     embed()
     tmp = LIB + ".tmp%d" % os.getpid()
-    objs = []
+    objs, running = [], []
     for src in HIP_SOURCES:
-        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
         hcmd = [os.path.join(ROCM, "bin", "hipcc")] + HIPCC_FLAGS + [
             "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(hcmd), flush=True)
-        subprocess.check_call(hcmd)
+        running.append((hcmd, subprocess.Popen(hcmd)))
         objs.append(obj)
+    failed = [subprocess.CalledProcessError(p.returncode, c) for c, p in running if p.wait() != 0]
+    if failed:
+        raise failed[0]
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-Wextra",
            "-Wno-unused-parameter", "-D__HIP_PLATFORM_AMD__",
            "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", BUILD,

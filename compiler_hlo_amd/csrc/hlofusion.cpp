@@ -18,6 +18,7 @@
 #include <string>
 #include <vector>
 
+#include "check.h"
 #include "ir.h"
 #include "plan.h"
 #include "scratch.h"
@@ -45,10 +46,7 @@ thread_local std::string t_err;
 
 void set_err(const std::string &m) { t_err = m; }
 
-hf_status hip_fail(hipError_t e, const char *what) {
-  set_err(std::string(what) + ": " + hipGetErrorString(e));
-  return HF_ERR_HIP;
-}
+hf_status hip_fail(hipError_t e, const char *what) { return hf::hip_error(e, what); }
 
 const char *hero_text(hf_hero h) {
   switch (h) {
@@ -272,35 +270,8 @@ hf_status launch(hf_fusion *f, const void *const *params, int32_t n_params, void
     set_err("the current device differs from the device the fusion was created on");
     return HF_ERR_INVALID;
   }
-  // A buffer must be device memory of this device (or managed memory), with
-  // its whole extent inside one allocation: anything else is rejected here,
-  // before a kernel could fault on it.
   auto check_buffer = [&](const void *p, size_t bytes, const std::string &what) -> bool {
-    hipPointerAttribute_t a;
-    if (hipPointerGetAttributes(&a, p) != hipSuccess) {
-      (void)hipGetLastError();  // do not leave the failed query to the next call
-      set_err(what + " is not device memory");
-      return false;
-    }
-    const bool managed = a.isManaged || a.type == hipMemoryTypeManaged;
-    if (!managed && (a.type != hipMemoryTypeDevice || a.device != f->device)) {
-      set_err(what + " is not device memory of the fusion's device");
-      return false;
-    }
-    if (!managed) {
-      hipDeviceptr_t base = nullptr;
-      size_t size = 0;
-      if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)p) != hipSuccess) {
-        (void)hipGetLastError();
-        set_err(what + ": hipMemGetAddressRange failed");
-        return false;
-      }
-      if ((uintptr_t)p + bytes > (uintptr_t)base + size) {
-        set_err(what + " extends past the end of its allocation");
-        return false;
-      }
-    }
-    return true;
+    return hf::check_buffer(p, bytes, f->device, "fusion", what);
   };
   const hf::Type &rt = f->g.nodes[f->g.root].t;
   const size_t rbytes = (size_t)hf::storage_bytes(rt.dt, rt.numel());
@@ -381,6 +352,41 @@ hf_status launch(hf_fusion *f, const void *const *params, int32_t n_params, void
 }  // namespace
 
 namespace hf {
+
+void set_error(const std::string &m) { set_err(m); }
+
+hf_status hip_error(hipError_t e, const char *what) {
+  set_err(std::string(what) + ": " + hipGetErrorString(e));
+  return HF_ERR_HIP;
+}
+
+bool check_buffer(const void *p, size_t bytes, int device, const char *owner, const std::string &what) {
+  hipPointerAttribute_t a;
+  if (hipPointerGetAttributes(&a, p) != hipSuccess) {
+    (void)hipGetLastError();  // do not leave the failed query to the next call
+    set_err(what + " is not device memory");
+    return false;
+  }
+  const bool managed = a.isManaged || a.type == hipMemoryTypeManaged;
+  if (!managed && (a.type != hipMemoryTypeDevice || a.device != device)) {
+    set_err(what + " is not device memory of the " + owner + "'s device");
+    return false;
+  }
+  if (!managed) {
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)p) != hipSuccess) {
+      (void)hipGetLastError();
+      set_err(what + ": hipMemGetAddressRange failed");
+      return false;
+    }
+    if ((uintptr_t)p + bytes > (uintptr_t)base + size) {
+      set_err(what + " extends past the end of its allocation");
+      return false;
+    }
+  }
+  return true;
+}
 
 hf_status launch_in_scratch(hf_fusion *f, const void *const *params, int32_t n_params, void *result, void *stream) {
   if (!f) {

@@ -1,0 +1,698 @@
+// rows.hip -- the operators that are bound by memory: the root-mean-square
+// norm and its gradient, dropout, the activation's gradient, and the copies
+// that lay out an operand.
+#include "device.h"
+
+namespace hf {
+namespace {
+
+// Where element i of a thread's vector j lies in a row.  VEC: eight
+// consecutive elements a thread, so that each access is 16 bytes.  Otherwise
+// (rows that are not 16-byte aligned, or a length that is no multiple of 8)
+// consecutive threads take consecutive elements.
+template <int T, bool VEC>
+__device__ __forceinline__ int column(int t, int j, int i) {
+  return VEC ? (j * T + t) * 8 + i : (j * 8 + i) * T + t;
+}
+
+// One vector of a row; elements past the row's end are 0.
+template <class E, int T, bool VEC>
+__device__ __forceinline__ void load_row(const typename E::Store *row, int t, int j, int cols, float (&v)[8]) {
+  if (VEC) {
+    const int c = column<T, VEC>(t, j, 0);
+    if (c < cols) {
+      load8<E>(row + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<T, VEC>(t, j, i);
+      v[i] = c < cols ? E::load(row[c]) : 0.f;
+    }
+  }
+}
+
+template <class E, int T, bool VEC>
+__device__ __forceinline__ void store_row(typename E::Store *row, int t, int j, int cols, const float (&v)[8]) {
+  if (VEC) {
+    const int c = column<T, VEC>(t, j, 0);
+    if (c < cols) store8<E>(row + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<T, VEC>(t, j, i);
+      if (c < cols) row[c] = E::store(v[i]);
+    }
+  }
+}
+
+// The weight, in f32 or in the rows' type.
+template <class E, int T, bool VEC>
+__device__ __forceinline__ void load_weight(const void *w, bool wide, int t, int j, int cols, float (&v)[8]) {
+  if (wide)
+    load_row<F32, T, VEC>((const float *)w, t, j, cols, v);
+  else
+    load_row<E, T, VEC>((const typename E::Store *)w, t, j, cols, v);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+  return v;
+}
+
+// Over the T threads of a row.  `slots`: T/64 floats of this call's own (no
+// second barrier is needed before the next call, which takes other slots).
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float *slots) {
+  v = wave_sum(v);
+  if (T == 64) return v;
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x / 64] = v;
+  __syncthreads();
+  v = slots[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; ++i) v += slots[i];
+  return v;
+}
+
+// The largest magnitude of a row.  Magnitudes are compared as the integers
+// that their bits are: the same order, and a NaN is above infinity, so a row
+// that holds one gets it.
+template <int T>
+__device__ __forceinline__ float row_top(uint32_t v, uint32_t *slots) {
+  v = wave_max(v);
+  if (T != 64) {
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x / 64] = v;
+    __syncthreads();
+    v = slots[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) v = max(v, slots[i]);
+  }
+  return __uint_as_float(v);
+}
+
+// y / scale, rounded once, for every element of a row: r is the rounded
+// reciprocal, q = y r is within two ulps of the quotient and the remainder
+// y - q scale, exact in one fma, corrects it.  Where r or the remainder
+// could overflow (scales near the ends of the range, infinite or NaN) the
+// division itself is taken.
+struct Quotient {
+  float s, r;
+  bool slow;
+  __device__ __forceinline__ explicit Quotient(float scale) : s(scale), r(1.0f / scale), slow(!(scale > 1e-30f && scale < 1e30f)) {}
+  __device__ __forceinline__ float operator()(float y) const {
+    if (slow) return s == 0.f ? 0.f : y / s;
+    const float q = y * r;
+    return __builtin_fmaf(__builtin_fmaf(-q, s, y), r, q);
+  }
+};
+
+// Eight quotients as e4m3 or s8, each rounded to nearest even and clamped.
+// NaN stays NaN in e4m3 and is 0 in s8, which has none.
+template <int OUT>
+__device__ __forceinline__ u32x2 pack8(const float (&v)[8]) {
+  u32x2 r;
+  if (OUT == HF_F8E4M3) {
+    float c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = v[i] != v[i] ? v[i] : __builtin_fminf(__builtin_fmaxf(v[i], -448.f), 448.f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h], c[4 * h + 1], 0, false);
+      r[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h + 2], c[4 * h + 3], w, true);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = v[4 * h + i];
+        const int q = f != f ? 0 : (int)__builtin_rintf(__builtin_fminf(__builtin_fmaxf(f, -127.f), 127.f));
+        w |= (uint32_t)(q & 0xff) << (8 * i);
+      }
+      r[h] = w;
+    }
+  }
+  return r;
+}
+
+template <int OUT, int T, bool VEC>
+__device__ __forceinline__ void store_row8(uint8_t *row, int t, int j, int cols, const float (&v)[8]) {
+  const u32x2 p = pack8<OUT>(v);
+  if (VEC) {
+    const int c = column<T, VEC>(t, j, 0);
+    if (c < cols) *(u32x2 *)(row + c) = p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<T, VEC>(t, j, i);
+      if (c < cols) row[c] = (uint8_t)(p[i / 4] >> (8 * (i % 4)));
+    }
+  }
+}
+
+// RmsNorm.  h = x + residual in f32; rstd = (mean h^2 + eps)^-1/2;
+// y = h rstd weight, rounded once; in 8 bits, scale = max|y| / Q of the row
+// and q = y / scale.  The row stays in registers between its sum, its largest
+// magnitude and its store, so x and residual are read once: the kernel is
+// bound by memory.  T threads a row; a row of 1024 elements or fewer is one
+// wave's, and a workgroup then takes four.
+// NV = 0: rows too long for registers, read again for each of the steps.
+template <class E, int OUT, int T, int NV, bool VEC>
+__global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a) {
+  __shared__ float slots[T == 64 ? 1 : T / 64];
+  __shared__ uint32_t top_slots[T == 64 ? 1 : T / 64];
+  __shared__ float far_slots[T == 64 ? 1 : T / 64];
+  __shared__ uint32_t far_top_slots[T == 64 ? 1 : T / 64];
+  constexpr int ROWS = T == 64 ? 4 : 1;
+  const int t = threadIdx.x % T;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / T;
+  if (row >= a.rows) return;  // whole waves, and no barrier follows where ROWS > 1
+  typedef typename E::Store S;
+  const S *x = (const S *)a.x + row * a.ldx;
+  const S *r = a.residual ? (const S *)a.residual + row * a.ldr : nullptr;
+  S *stream = a.stream ? (S *)a.stream + row * a.lds : nullptr;
+  const int n = NV ? NV : (a.cols + 8 * T - 1) / (8 * T);
+  float keep[NV ? NV : 1][8];
+  float sum = 0.f;
+  auto input = [&](int j, float (&h)[8]) {
+    load_row<E, T, VEC>(x, t, j, a.cols, h);
+    if (r) {
+      float o[8];
+      load_row<E, T, VEC>(r, t, j, a.cols, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] += o[i];
+    }
+  };
+  auto take = [&](int j, float (&h)[8]) {
+    input(j, h);
+    if (stream) store_row<E, T, VEC>(stream, t, j, a.cols, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[i], h[i], sum);
+  };
+  if (NV) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) take(j, keep[j]);
+  } else {
+    for (int j = 0; j < n; ++j) take(j, keep[0]);
+  }
+  sum = row_sum<T>(sum, slots);
+  const float m = sum / (float)a.cols + a.eps;
+  // v_rsq is within one ulp; the step brings it to half an ulp and a bit
+  float rstd = __builtin_amdgcn_rsqf(m);
+  if (m > 1e-30f && m < 1e37f) {
+    const float e = __builtin_fmaf(-m * rstd, rstd, 1.f);
+    rstd = __builtin_fmaf(0.5f * rstd, e, rstd);
+  } else {
+    // The squares may have left the range of 32 bits though rstd is in it:
+    // once more, with the row scaled by a power of two that brings its
+    // largest magnitude (or sqrt(eps), where that is larger) to 1 .. 2.
+    uint32_t top = 0;
+    auto widen = [&](const float (&h)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(h[i]) & 0x7fffffffu);
+    };
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) widen(keep[j]);
+    } else {
+      for (int j = 0; j < n; ++j) {
+        input(j, keep[0]);
+        widen(keep[0]);
+      }
+    }
+    float root = sqrtf(a.eps);
+    const float largest = __builtin_fmaxf(row_top<T>(top, far_top_slots), root);
+    int power = 0;
+    (void)frexpf(largest, &power);
+    const bool far = largest > 0.f && largest < __builtin_inff();
+    float again = 0.f;
+    auto add = [&](const float (&h)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = ldexpf(h[i], 1 - power);
+        again = __builtin_fmaf(v, v, again);
+      }
+    };
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) add(keep[j]);
+    } else {
+      for (int j = 0; j < n; ++j) {
+        input(j, keep[0]);
+        add(keep[0]);
+      }
+    }
+    again = row_sum<T>(again, far_slots);
+    root = ldexpf(root, 1 - power);
+    rstd = far ? ldexpf(1.0f / sqrtf(again / (float)a.cols + root * root), 1 - power) : 1.0f / sqrtf(m);
+  }
+  if (a.rstd && t == 0) a.rstd[row] = rstd;
+  const bool wide = a.weight_dtype == HF_F32;
+  auto scaled = [&](int j, float (&h)[8]) {
+    float w[8];
+    load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = h[i] * rstd * w[i];
+  };
+  if (OUT < 0) {
+    S *y = (S *)a.y + row * a.ldy;
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        scaled(j, keep[j]);
+        store_row<E, T, VEC>(y, t, j, a.cols, keep[j]);
+      }
+    } else {
+      for (int j = 0; j < n; ++j) {
+        input(j, keep[0]);
+        scaled(j, keep[0]);
+        store_row<E, T, VEC>(y, t, j, a.cols, keep[0]);
+      }
+    }
+  } else {
+    uint32_t top = 0;
+    auto widen = [&](const float (&h)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(h[i]) & 0x7fffffffu);
+    };
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        scaled(j, keep[j]);
+        widen(keep[j]);
+      }
+    } else {
+      for (int j = 0; j < n; ++j) {
+        input(j, keep[0]);
+        scaled(j, keep[0]);
+        widen(keep[0]);
+      }
+    }
+    const float scale = row_top<T>(top, top_slots) / (OUT == HF_F8E4M3 ? 448.f : 127.f);
+    if (t == 0) a.scale[row] = scale;
+    const Quotient q(scale);
+    uint8_t *y = (uint8_t *)a.y + row * a.ldy;
+    auto out = [&](int j, float (&h)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = q(h[i]);
+      store_row8<OUT, T, VEC>(y, t, j, a.cols, h);
+    };
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) out(j, keep[j]);
+    } else {
+      for (int j = 0; j < n; ++j) {
+        input(j, keep[0]);
+        scaled(j, keep[0]);
+        out(j, keep[0]);
+      }
+    }
+  }
+}
+
+// RmsNormGrad.  With xh = h rstd and g = dy weight,
+//   dx = (g - xh mean(g xh)) rstd + dstream,   dweight = sum over rows dy xh.
+// A workgroup (one wave in rows of 1024 or fewer) takes every groups-th row
+// and keeps its columns' dweight in registers over all of them, so dweight
+// costs no memory traffic but one partial row a group; fold_kernel adds the
+// groups in a fixed order.  Bound by memory: dy, h and dstream read once, dx
+// written once.
+template <class E, int T, int NV, bool VEC>
+__global__ __launch_bounds__(T == 64 ? 256 : T) void norm_grad_kernel(NormGradArgs a) {
+  __shared__ float slots[2][T == 64 ? 1 : T / 64];
+  constexpr int PER = T == 64 ? 4 : 1;
+  const int t = threadIdx.x % T;
+  const int group = blockIdx.x * PER + threadIdx.x / T;
+  if (group >= a.groups) return;
+  typedef typename E::Store S;
+  const bool wide = a.weight_dtype == HF_F32;
+  const int n = NV ? NV : (a.cols + 8 * T - 1) / (8 * T);
+  constexpr int K = NV ? NV : 1;
+  float *partial = a.partial + (int64_t)group * a.cols;
+  float dw[K][8], w[K][8];
+  if (NV) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+    }
+  } else {
+    for (int j = 0; j < n; ++j) {
+      float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      store_row<F32, T, VEC>(partial, t, j, a.cols, z);
+    }
+  }
+  int turn = 0;
+  for (int64_t row = group; row < a.rows; row += a.groups, turn ^= 1) {
+    const S *dy = (const S *)a.dy + row * a.lddy, *h = (const S *)a.h + row * a.ldh;
+    const S *ds = a.dstream ? (const S *)a.dstream + row * a.ldds : nullptr;
+    S *dx = (S *)a.dx + row * a.lddx;
+    const float rstd = a.rstd[row];
+    float xh[K][8], g[K][8], o[K][8];
+    float dot = 0.f;
+    auto take = [&](int j, int k) {
+      load_row<E, T, VEC>(h, t, j, a.cols, xh[k]);
+      load_row<E, T, VEC>(dy, t, j, a.cols, g[k]);
+      if (!NV) load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w[k]);
+    };
+    auto join = [&](int k, bool grad) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xh[k][i] *= rstd;
+        if (grad) dw[k][i] = __builtin_fmaf(g[k][i], xh[k][i], dw[k][i]);
+        g[k][i] *= w[k][i];
+        dot = __builtin_fmaf(g[k][i], xh[k][i], dot);
+      }
+    };
+    auto put = [&](int j, int k, float mean) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[k][i] = (g[k][i] - xh[k][i] * mean) * rstd;
+        if (ds) g[k][i] += o[k][i];
+      }
+      store_row<E, T, VEC>(dx, t, j, a.cols, g[k]);
+    };
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) take(j, j);
+      if (ds) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) load_row<E, T, VEC>(ds, t, j, a.cols, o[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) join(j, true);
+    } else {
+      for (int j = 0; j < n; ++j) {
+        take(j, 0);
+        load_row<F32, T, VEC>(partial, t, j, a.cols, dw[0]);
+        join(0, true);
+        store_row<F32, T, VEC>(partial, t, j, a.cols, dw[0]);
+      }
+    }
+    // the slots change with each row: a thread may be one row ahead of
+    // another, never two, as each row has a barrier
+    const float mean = row_sum<T>(dot, slots[turn]) / (float)a.cols;
+    if (NV) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) put(j, j, mean);
+    } else {
+      for (int j = 0; j < n; ++j) {
+        take(j, 0);
+        if (ds) load_row<E, T, VEC>(ds, t, j, a.cols, o[0]);
+        join(0, false);
+        put(j, 0, mean);
+      }
+    }
+  }
+  if (NV) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) store_row<F32, T, VEC>(partial, t, j, a.cols, dw[j]);
+  }
+}
+
+// out[c] = sum over g of partial[g][c], always in the same order: 32 columns
+// a workgroup, 8 threads a column.
+__global__ __launch_bounds__(256) void fold_kernel(const float *partial, int groups, int64_t cols, float *out) {
+  __shared__ float part[8][32];
+  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+  const int lane = threadIdx.x / 32;
+  float s = 0.f;
+  if (c < cols)
+    for (int g = lane; g < groups; g += 8) s += partial[(int64_t)g * cols + c];
+  part[lane][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (lane == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
+    out[c] = s;
+  }
+}
+
+// Dropout.  Element i of the row-major array takes 16 bits of the generator's
+// call number offset + i / 8: word (i % 8) / 2, the low half for even i.  It
+// is kept where they are >= cut = p 65536, so the kept share is exactly
+// 1 - cut / 65536 and scale its exact inverse.  One call serves one 16-byte
+// vector; nothing of the mask is stored, and the backward pass makes it again.
+// Bound by memory in bf16 and f16 as measured: 20 32x32-bit products a
+// vector.
+template <class E, bool VEC>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a) {
+  typedef typename E::Store S;
+  const uint64_t key = (uint64_t)a.state[0], offset = (uint64_t)a.state[1];
+  const int64_t total = a.rows * a.cols, vectors = (total + 7) / 8;
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (v >= vectors) return;
+  const u32x4 word = philox(offset + (uint64_t)v, key);
+  // arrays without gaps come as one row
+  int64_t row = 0, col = v * 8;
+  if (a.rows > 1) {
+    row = (v * 8) / a.cols;
+    col = v * 8 - row * a.cols;
+  }
+  auto kept = [&](int i, float x) {
+    const uint32_t bits = i % 2 ? word[i / 2] >> 16 : word[i / 2] & 0xffff;
+    return bits >= a.cut ? x * a.scale : 0.f;
+  };
+  if (VEC && v * 8 + 8 <= total) {
+    float x[8], r[8];
+    load8<E>((const S *)a.x + row * a.ldx + col, x);
+    if (a.residual) load8<E>((const S *)a.residual + row * a.ldr + col, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = kept(i, x[i]) + (a.residual ? r[i] : 0.f);
+    store8<E>((S *)a.y + row * a.ldy + col, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (v * 8 + i < total) {
+        float x = kept(i, E::load(((const S *)a.x)[row * a.ldx + col]));
+        if (a.residual) x += E::load(((const S *)a.residual)[row * a.ldr + col]);
+        ((S *)a.y)[row * a.ldy + col] = E::store(x);
+        if (++col == a.cols) col = 0, ++row;
+      }
+    }
+  }
+}
+
+// dz = dd act'(z) in the operands' type, and the column sums' partials from
+// the values before that rounding.  256 threads take 8 columns each of every
+// groups-th row.  Columns n .. lddz-1 of dz are padding and become 0, so that
+// a product over them adds nothing.
+template <class E, bool GATED, bool VEC>
+__global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
+  typedef typename E::Store S;
+  const int64_t c0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  // GATED: both halves' columns lie side by side, so padding follows 2n
+  const int64_t width = GATED ? (int64_t)a.n : (a.dz ? a.lddz : (int64_t)a.n);
+  if (c0 >= width) return;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t row = blockIdx.y; row < a.m; row += a.groups) {
+    const S *dd = (const S *)a.dd + row * a.lddd;
+    const S *z = a.z ? (const S *)a.z + row * a.ldz : nullptr;
+    S *dz = a.dz ? (S *)a.dz + row * a.lddz : nullptr;
+    float d[8], g[8], u[8];
+    auto get = [&](const S *p, float (&v)[8]) {
+      if (VEC) {
+        load8<E>(p + c0, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c0 + i < a.n ? E::load(p[c0 + i]) : 0.f;
+      }
+    };
+    auto set = [&](S *p, int64_t extent, const float (&v)[8]) {
+      if (VEC) {
+        store8<E>(p + c0, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + i < extent) p[c0 + i] = E::store(v[i]);
+      }
+    };
+    get(dd, d);
+    if (GATED) {
+      get(z, g);
+      get(z + a.n, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float f, df;
+        f = act_both(a.act, g[i], &df);
+        g[i] = d[i] * u[i] * df;
+        u[i] = d[i] * f;
+      }
+      set(dz, a.n, g);
+      set(dz + a.n, a.n, u);
+      if (c0 + 8 >= a.n)
+        for (int64_t c = 2 * (int64_t)a.n; c < a.lddz; ++c) dz[c] = E::store(0.f);
+    } else {
+      if (z) {
+        get(z, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float df;
+          (void)act_both(a.act, g[i], &df);
+          d[i] *= df;
+        }
+      }
+      if (dz) set(dz, a.lddz, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += d[i];
+    }
+  }
+  if (!GATED && a.partial) {
+    float *p = a.partial + (int64_t)blockIdx.y * a.n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < a.n) p[c0 + i] = sum[i];
+  }
+}
+
+// Rows of any alignment into rows that start on 16 bytes, the tail zero.
+template <class S>
+__global__ __launch_bounds__(256) void pack_kernel(const S *src, int64_t ld_src, S *dst, int64_t ld_dst, int64_t rows,
+                                                   int64_t cols) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= ld_dst) return;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ld_dst + c] = c < cols ? src[r * ld_src + c] : (S)0;
+}
+
+template <class E, int OUT, int T, int NV>
+void norm_go(const NormArgs &a, hipStream_t s) {
+  const int per = T == 64 ? 4 : 1;
+  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+  const unsigned block = T == 64 ? 256 : T;
+  if (a.vec)
+    norm_kernel<E, OUT, T, NV, true><<<grid, block, 0, s>>>(a);
+  else
+    norm_kernel<E, OUT, T, NV, false><<<grid, block, 0, s>>>(a);
+}
+
+template <class E, int OUT>
+void norm_by_length(const NormArgs &a, hipStream_t s) {
+  if (a.cols <= 512) norm_go<E, OUT, 64, 1>(a, s);
+  else if (a.cols <= 1024) norm_go<E, OUT, 64, 2>(a, s);
+  else if (a.cols <= 2048) norm_go<E, OUT, 256, 1>(a, s);
+  else if (a.cols <= 4096) norm_go<E, OUT, 256, 2>(a, s);
+  else if (a.cols <= 8192) norm_go<E, OUT, 256, 4>(a, s);
+  else if (a.cols <= 16384) norm_go<E, OUT, 1024, 2>(a, s);
+  else if (a.cols <= 32768) norm_go<E, OUT, 1024, 4>(a, s);
+  else norm_go<E, OUT, 1024, 0>(a, s);
+}
+
+template <class E>
+void norm_by_out(const NormArgs &a, hipStream_t s) {
+  if (a.out_dtype == HF_F8E4M3) norm_by_length<E, HF_F8E4M3>(a, s);
+  else if (a.out_dtype == HF_S8) norm_by_length<E, HF_S8>(a, s);
+  else norm_by_length<E, -1>(a, s);
+}
+
+template <class E, int T, int NV>
+void norm_grad_go(const NormGradArgs &a, hipStream_t s) {
+  const int per = T == 64 ? 4 : 1;
+  const unsigned grid = (unsigned)((a.groups + per - 1) / per);
+  const unsigned block = T == 64 ? 256 : T;
+  if (a.vec)
+    norm_grad_kernel<E, T, NV, true><<<grid, block, 0, s>>>(a);
+  else
+    norm_grad_kernel<E, T, NV, false><<<grid, block, 0, s>>>(a);
+}
+
+template <class E>
+void norm_grad_by_length(const NormGradArgs &a, hipStream_t s) {
+  if (a.cols <= 512) norm_grad_go<E, 64, 1>(a, s);
+  else if (a.cols <= 1024) norm_grad_go<E, 64, 2>(a, s);
+  else if (a.cols <= 2048) norm_grad_go<E, 256, 1>(a, s);
+  else if (a.cols <= 4096) norm_grad_go<E, 256, 2>(a, s);
+  else if (a.cols <= 8192) norm_grad_go<E, 1024, 1>(a, s);
+  else if (a.cols <= 16384) norm_grad_go<E, 1024, 2>(a, s);
+  else norm_grad_go<E, 1024, 0>(a, s);
+}
+
+template <class E>
+void dropout_go(const DropoutArgs &a, hipStream_t s) {
+  const int64_t vectors = (a.rows * a.cols + 7) / 8;
+  const unsigned grid = (unsigned)((vectors + 255) / 256);
+  if (a.vec)
+    dropout_kernel<E, true><<<grid, 256, 0, s>>>(a);
+  else
+    dropout_kernel<E, false><<<grid, 256, 0, s>>>(a);
+}
+
+template <class E>
+void act_grad_go(const ActGradArgs &a, hipStream_t s) {
+  const int64_t width = a.gated || !a.dz ? (int64_t)a.n : a.lddz;
+  const dim3 grid((unsigned)((width + 2047) / 2048), (unsigned)a.groups);
+  if (a.gated && a.vec) act_grad_kernel<E, true, true><<<grid, 256, 0, s>>>(a);
+  else if (a.gated) act_grad_kernel<E, true, false><<<grid, 256, 0, s>>>(a);
+  else if (a.vec) act_grad_kernel<E, false, true><<<grid, 256, 0, s>>>(a);
+  else act_grad_kernel<E, false, false><<<grid, 256, 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
+  if (a.dtype == HF_BF16) norm_by_out<BF16>(a, s);
+  else if (a.dtype == HF_F16) norm_by_out<F16>(a, s);
+  else norm_by_out<F32>(a, s);
+  return hipGetLastError();
+}
+
+int norm_grad_groups(int64_t rows, int64_t cols) {
+  // enough workgroups for the memory to be kept busy (4 of 256 threads a
+  // compute unit, 2 of 1024), and no more partial rows than that
+  const int64_t most = cols <= 1024 ? 4096 : cols <= 4096 ? 1024 : 512;
+  return (int)(rows < 1 ? 1 : rows < most ? rows : most);
+}
+
+hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
+  if (a.dtype == HF_BF16) norm_grad_by_length<BF16>(a, s);
+  else if (a.dtype == HF_F16) norm_grad_by_length<F16>(a, s);
+  else norm_grad_by_length<F32>(a, s);
+  hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_column_fold(a.partial, a.groups, a.cols, a.dweight, s);
+}
+
+hipError_t launch_column_fold(const float *partial, int groups, int64_t cols, float *out, hipStream_t s) {
+  fold_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(partial, groups, cols, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_dropout(const DropoutArgs &a, hipStream_t s) {
+  if (a.dtype == HF_BF16) dropout_go<BF16>(a, s);
+  else if (a.dtype == HF_F16) dropout_go<F16>(a, s);
+  else dropout_go<F32>(a, s);
+  return hipGetLastError();
+}
+
+int act_grad_groups(int64_t m, int64_t n) {
+  const int64_t wide = (n + 2047) / 2048;
+  const int64_t most = wide >= 64 ? 64 : 4096 / (wide > 0 ? wide : 1) < 512 ? 4096 / (wide > 0 ? wide : 1) : 512;
+  return (int)(m < 1 ? 1 : m < most ? m : most);
+}
+
+hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s) {
+  if (a.dtype == HF_BF16) act_grad_go<BF16>(a, s);
+  else act_grad_go<F16>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_pack(const void *src, int64_t ld_src, void *dst, int64_t ld_dst, int64_t rows, int64_t cols,
+                       int elem_bytes, hipStream_t s) {
+  const dim3 grid((unsigned)((ld_dst + 255) / 256), (unsigned)(rows < 4096 ? rows : 4096));
+  if (elem_bytes == 1)
+    pack_kernel<uint8_t><<<grid, 256, 0, s>>>((const uint8_t *)src, ld_src, (uint8_t *)dst, ld_dst, rows, cols);
+  else
+    pack_kernel<uint16_t><<<grid, 256, 0, s>>>((const uint16_t *)src, ld_src, (uint16_t *)dst, ld_dst, rows, cols);
+  return hipGetLastError();
+}
+
+}  // namespace hf

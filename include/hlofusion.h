@@ -340,6 +340,161 @@ hf_status hf_fusion_launch_noalloc(hf_fusion *f, const void *const *params, int3
  * again later. */
 hf_status hf_fusion_destroy(hf_fusion *f);
 
+/* ------------------------------------------------------------------------
+ * Operators: the contractions, row norms and generators of a transformer's
+ * feed-forward layer, which no single hero covers.  They share the fusions'
+ * conventions (caller-owned device buffers, streams and workspace, statuses,
+ * hf_last_error, immutable handles bound to the device of their creation),
+ * with two differences: their kernels are compiled with the library, so
+ * creating one costs no compile, and a matrix may have a row stride larger
+ * than its row (elements of a row are always adjacent).
+ *
+ * Products and sums are held in 32 bits; every result is rounded to its type
+ * once, to nearest even.  [r, c] is a row-major matrix of r rows.
+ *
+ * HF_OPERATOR_RMS_NORM       h = x + residual; rstd = (mean(h^2) + epsilon)^(-1/2)
+ *   over a row's n elements; y = h * rstd * weight.  out_dtype HF_S8 or
+ *   HF_F8E4M3: scale = max|y| / Q of the row (Q = 127 or 448) and
+ *   y = round(y / scale), 0 in a row of zeros.  A row that holds a NaN has
+ *   scale NaN.
+ *     params  x [m, n] dtype, weight [n] weight_dtype, residual [m, n] (RESIDUAL)
+ *     results y [m, n] out_dtype, scale [m] f32 (8-bit out_dtype),
+ *             stream = h [m, n] dtype (RESIDUAL), rstd [m] f32
+ * HF_OPERATOR_RMS_NORM_GRAD  with xh = h * rstd and g = dy * weight:
+ *   dx = (g - xh * mean(g * xh)) * rstd + dstream, the gradient of x and of
+ *   residual alike; dweight = sum over rows of dy * xh.
+ *     params  dy [m, n], h [m, n] (x, or stream), weight [n], rstd [m] f32,
+ *             dstream [m, n] (RESIDUAL)
+ *     results dx [m, n], dweight [n] f32
+ * HF_OPERATOR_MATMUL         z = sum_k a[m, k] b[n, k] (* a_scale[m] * b_scale[n])
+ *   + bias[n]; d = activation(z) + residual.
+ *     params  a [m, k], b [n, k] dtype, a_scale [m], b_scale [n] f32 (8-bit dtype),
+ *             bias [n] out_dtype (BIAS), residual [m, n] out_dtype (RESIDUAL)
+ *     results d [m, n] out_dtype, z [m, n] out_dtype (SAVE)
+ * HF_OPERATOR_MATMUL_GRAD    dz = dd * activation'(z), rounded to dtype for the
+ *   products; da = dz b; db = dz^T a; dbias = column sums of dz (before that
+ *   rounding).  The residual's gradient is dd itself.
+ *     params  dd [m, n], a [m, k], b [n, k], z [m, n] (an activation)
+ *     results da [m, k], db [n, k] dtype, dbias [n] f32 (BIAS)
+ * HF_OPERATOR_GATED          the rows of b are n gate channels, then n up
+ *   channels: (g, u) = the two halves of z = a b^T (with scales as above);
+ *   d = activation(g) * u.
+ *     params  a [m, k], b [2n, k] dtype, a_scale [m], b_scale [2n] f32 (8-bit dtype)
+ *     results d [m, n] out_dtype, z [m, 2n] out_dtype (SAVE)
+ * HF_OPERATOR_GATED_GRAD     dz = (dd * u * activation'(g), dd * activation(g)),
+ *   rounded to dtype; da = dz b; db = dz^T a.
+ *     params  dd [m, n], a [m, k], b [2n, k], z [m, 2n]
+ *     results da [m, k], db [2n, k] dtype
+ * HF_OPERATOR_DROPOUT        y = keep * x / (1 - p) + residual.  Element i of the
+ *   row-major [m, n] takes 16 bits of call number offset + i / 8 of
+ *   Philox4x32-10 with key seed (word i % 8 / 2, low half first) and is kept
+ *   where they are >= cut = round(p * 65536); 1 - p is taken as
+ *   1 - cut / 65536, so the expectation is exact.  The backward pass is the
+ *   same operator, without residual, on the gradient with the same state.
+ *     params  x [m, n], state [2] s64 (seed, offset; read by the kernel, so a
+ *             captured launch can be replayed with another), residual [m, n] (RESIDUAL)
+ *     results y [m, n]
+ *
+ * dtype: bf16, f16 and f32 for the row operators and dropout; bf16, f16, s8
+ * and f8e4m3 for the products (gradients: bf16 and f16).  out_dtype: bf16,
+ * f16 or f32; for the norm also dtype itself, s8 or f8e4m3.  weight_dtype:
+ * dtype or f32.  m, n and k may be 0 (a norm needs n >= 1).  s8 products need
+ * k < 2^17, so that their 32-bit sums are exact. */
+typedef enum {
+  HF_OPERATOR_RMS_NORM = 0,
+  HF_OPERATOR_RMS_NORM_GRAD = 1,
+  HF_OPERATOR_MATMUL = 2,
+  HF_OPERATOR_MATMUL_GRAD = 3,
+  HF_OPERATOR_GATED = 4,
+  HF_OPERATOR_GATED_GRAD = 5,
+  HF_OPERATOR_DROPOUT = 6
+} hf_operator_kind;
+
+/* Element types beside hf_dtype's that operators take: the 8-bit float with 4
+ * exponent bits (finite range +-448, one NaN, no infinity), and the 64-bit
+ * integers of a generator's state. */
+typedef enum {
+  HF_F8E4M3 = 8,
+  HF_S64 = 9
+} hf_operator_dtype;
+
+/* gelu is its tanh form: 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+typedef enum {
+  HF_ACTIVATION_NONE = 0,
+  HF_ACTIVATION_RELU = 1,
+  HF_ACTIVATION_GELU = 2,
+  HF_ACTIVATION_SILU = 3
+} hf_activation;
+
+#define HF_OPERATOR_RESIDUAL 1u
+#define HF_OPERATOR_BIAS 2u
+#define HF_OPERATOR_SAVE 4u
+#define HF_MAX_OPERATOR_BUFFERS 10
+
+typedef struct {
+  int32_t abi_version;       /* HF_ABI_VERSION */
+  int32_t kind;              /* an hf_operator_kind value */
+  int64_t m, n, k;           /* k: products only, else 0 */
+  int32_t dtype;
+  int32_t out_dtype;         /* norm and products; gradients and dropout: dtype */
+  int32_t weight_dtype;      /* norm and its gradient; else ignored */
+  int32_t activation;        /* an hf_activation value (products; else 0) */
+  uint32_t flags;            /* HF_OPERATOR_RESIDUAL | _BIAS | _SAVE, where listed above */
+  double epsilon;            /* norm: >= 0 */
+  double probability;        /* dropout: 0 <= p < 1 */
+  /* Elements from a matrix row to the next, of each buffer in the order
+   * above (params, then results); 0: dense.  Vectors: 0. */
+  int64_t row_stride[HF_MAX_OPERATOR_BUFFERS];
+} hf_operator_desc;
+
+typedef struct {
+  int32_t dtype;
+  int32_t rank;              /* 1 or 2 */
+  int64_t dims[2];
+  int64_t row_stride;        /* rank 2 */
+} hf_buffer_info;
+
+typedef struct {
+  int32_t n_params, n_results;
+  hf_buffer_info buffers[HF_MAX_OPERATOR_BUFFERS];  /* params, then results */
+  int64_t workspace_bytes;
+  int64_t algorithmic_bytes; /* every param read once, every result written once */
+  int64_t algorithmic_flops; /* of the products; 0 for the others */
+  /* the (first) product: rows and columns of a workgroup's tile of sums, and
+   * the parts into which the contraction is split over workgroups; 0 without */
+  int32_t tile_rows, tile_cols, splits;
+} hf_operator_info;
+
+typedef struct hf_operator hf_operator;
+
+/* Validate and plan.  flags: 0, or HF_CREATE_PLAN_ONLY /
+ * HF_CREATE_COMPILE_ONLY (both: no GPU is touched and the handle cannot be
+ * launched).  Errors: HF_ERR_INVALID, HF_ERR_UNSUPPORTED (among them a row
+ * stride of 8 MB or more in a product's operand), HF_ERR_HIP, HF_ERR_NOMEM. */
+hf_status hf_operator_create(const hf_operator_desc *desc, uint32_t flags, hf_operator **out);
+
+/* Copy the plan into *info. */
+hf_status hf_operator_plan(const hf_operator *op, hf_operator_info *info);
+
+/* Run the operator on `stream`: asynchronous, no allocation, no
+ * synchronisation.  Buffers are checked as by hf_fusion_launch: non-NULL
+ * (unless empty), 16-byte aligned, device memory of the operator's device
+ * whose extent lies in one allocation, no result overlapping another buffer
+ * (column windows of one array with equal row strides do not overlap), and a
+ * workspace of workspace_bytes. */
+hf_status hf_operator_launch(const hf_operator *op, const void *const *params, int32_t n_params,
+                             void *const *results, int32_t n_results, void *workspace, void *stream);
+
+/* The same launch with the library's scratch memory as the workspace; see
+ * hf_fusion_launch_noalloc.  HF_ERR_UNSUPPORTED if workspace_bytes exceeds
+ * HF_SCRATCH_BYTES. */
+hf_status hf_operator_launch_noalloc(const hf_operator *op, const void *const *params, int32_t n_params,
+                                     void *const *results, int32_t n_results, void *stream);
+
+/* Release the handle (NULL is allowed).  It holds no device memory: launches
+ * in flight and captured graphs are not affected. */
+hf_status hf_operator_destroy(hf_operator *op);
+
 /* Message of the last failing call on this thread ("" if none). */
 const char *hf_last_error(void);
 
