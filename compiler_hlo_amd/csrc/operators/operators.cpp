@@ -160,7 +160,9 @@ void choose(hf_operator &op, Product &p, int64_t elem) {
   } else {
     const int64_t steps = cdiv(p.k, 128 / elem);
     auto tiles = [&](int64_t t) { return cdiv(p.m, t) * cdiv(p.n, p.gated ? t / 2 : t); };
-    p.tile = tiles(256) >= 192 ? 0 : 1;
+    // e4m3 widened to 16 bits has no registers to spare for the larger tile
+    const bool wide = op.d.dtype == HF_F8E4M3 && f8_wide(op.d.out_dtype, p.k);
+    p.tile = tiles(256) >= 192 && !wide ? 0 : 1;
     int64_t s = 1;
     if (p.tile == 1)
       while (tiles(128) * s < 256 && steps >= 8 * s) s *= 2;

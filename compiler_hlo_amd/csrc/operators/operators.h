@@ -102,6 +102,8 @@ struct ProductArgs {
   Epilogue e;
 };
 hipError_t launch_product(const ProductArgs &a, hipStream_t s);
+// Which e4m3 products go through f16 (StepF8Wide).
+constexpr bool f8_wide(int out_dtype, int64_t k) { return out_dtype == HF_F32 || k <= 128; }
 
 struct SkinnyArgs {
   ProductArgs p;             // splits: workgroups over k

@@ -8,9 +8,45 @@ typedef __attribute__((address_space(3))) char lds_char;
 
 // A view of an operand from a byte on, as the buffer loads want it: they
 // return zeros past the operand's end, so ragged edges need no branch.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const char *p, int64_t left) {
-  const int64_t n = left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left;
-  return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)n, 0x00020000);
+__device__ __forceinline__ i32x4 view(const char *p, int64_t left) {
+  const uint64_t at = (uint64_t)p;
+  // in 32-bit halves, so that it stays in scalar instructions
+  const int hi = (int)(left >> 32), lo = (int)(uint32_t)left;
+  i32x4 r;
+  r[0] = (int)(uint32_t)at;
+  r[1] = (int)(uint32_t)(at >> 32) & 0xffff;
+  r[2] = hi < 0 ? 0 : (hi > 0 || lo < 0) ? 0x7fffffff : lo;
+  r[3] = 0x00020000;
+  return r;
+}
+
+// 16 bytes a lane from `r` at byte v + at (past its end: zeros) into LDS, lane
+// l at lds + 16 l.  The load has no register result; it is counted by vmcnt alone,
+// and whoever reads the bytes waits for the count first and then meets the
+// other waves at a barrier.  It is written as assembly because the compiler
+// makes every LDS read after the builtin wait for all loads in flight.  m0,
+// which the compiler gives to nothing (no LDS access of this target needs it),
+// holds the LDS address.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, i32x4 r, uint32_t v, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(v), "s"(r), "s"(at)
+               : "memory");
+}
+
+// All loads but the newest N have arrived, and this wave's LDS reads.
+template <int N>
+__device__ __forceinline__ void arrived() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+}
+
+// A barrier that nothing is moved across; it waits for no memory by itself.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
 }
 
 // One half (R rows of the operand's tile, 128 bytes of the contraction) of a
@@ -56,30 +92,39 @@ struct Half {
     const int l = threadIdx.x % 64;
     return !COL && ((l & 7) ^ (l >> 3)) * 16 >= left ? 0x80000000u : 0u;
   }
-  static __device__ __forceinline__ void load(lds_char *lds, __amdgpu_buffer_rsrc_t r, const uint32_t (&v)[kLoads],
+  // into LDS from `lds` on (this wave's first kilobyte)
+  static __device__ __forceinline__ void load(uint32_t lds, i32x4 r, const uint32_t (&v)[kLoads], uint32_t at,
                                               uint32_t past) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (__attribute__((address_space(3))) void *)(lds + ((threadIdx.x / 64) + 8 * i) * 1024), 16, v[i] | past, 0,
-          0, 0);
+    for (int i = 0; i < kLoads; ++i) load_to_lds(lds + i * 8192, r, COL ? v[i] : v[i] | past, at);
   }
 
-  // The fragment of rows (by column: columns) base + 16 t + l % 16.
-  static __device__ __forceinline__ void read(const lds_char *lds, int base, int t, i32x4 (&f)[2]) {
-    const int l = threadIdx.x % 64;
-    if (!COL) {
-      const lds_char *p = lds + (base + t * 16 + (l & 15)) * 128;
-      f[0] = *(const __attribute__((address_space(3))) i32x4 *)(p + (((l >> 4) ^ (l & 7)) * 16));
-      f[1] = *(const __attribute__((address_space(3))) i32x4 *)(p + (((l >> 4) ^ (l & 7) ^ 4) * 16));
-    } else {
-      const int g = l >> 4, i = l & 15, s = (i >> 2) | (R == 128 ? (g & 1) << 2 : 0);
-      const lds_char *p = lds + (g * 8 + (i >> 2)) * (R * 2) + (((base / 16 + t) ^ s) * 32) + (i & 3) * 8;
+  // This lane's LDS addresses for the fragments of T tiles from row (column)
+  // `base` of the half on: one for each half of the contraction bytes by row,
+  // one for each tile by column.  Everything else is a constant.
+  template <int T>
+  static constexpr int kAddr = COL ? T : 2;
+  template <int T>
+  static __device__ __forceinline__ void addresses(uint32_t lds, int base, uint32_t (&p)[kAddr<T>]) {
+    const int l = threadIdx.x % 64, g = l >> 4, i = l & 15;
+    const int s = (i >> 2) | (R == 128 ? (g & 1) << 2 : 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int t = 0; t < kAddr<T>; ++t) {
+      p[t] = lds + (COL ? (g * 8 + (i >> 2)) * (R * 2) + (((base / 16 + t) ^ s) * 32) + (i & 3) * 8
+                        : (base + i) * 128 + ((g ^ (l & 7) ^ (t * 4)) * 16));
+    }
+  }
+  // The fragment of tile t: rows (columns) base + 16 t + l % 16.
+  template <int T>
+  static __device__ __forceinline__ void read(const uint32_t (&p)[kAddr<T>], uint32_t at, int t, i32x4 (&f)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!COL) {
+        f[h] = *(const __attribute__((address_space(3))) i32x4 *)(p[h] + at + t * 2048);
+      } else {
         typedef __attribute__((address_space(3))) i16x4 tr;
-        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(p + (h * 32) * (R * 2)));
-        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(p + (h * 32 + 4) * (R * 2)));
+        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(p[t % kAddr<T>] + at + h * (R * 64)));
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(p[t % kAddr<T>] + at + h * (R * 64) + R * 8));
         f[h] = __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
     }
@@ -148,48 +193,112 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
 #pragma unroll
         for (int y = 0; y < TN; ++y) acc[i][j][x][y] = typename Step::Acc{0, 0, 0, 0};
 
-  auto fetch = [&](int kt, char *stage) {
-    const char *pa = (const char *)a.a + a0 + kt * a_step, *pb = (const char *)a.b + b0 + kt * b_step;
-    const int64_t la = a.a_bytes - a0 - kt * a_step, lb = a.b_bytes - b0 - kt * b_step;
-    const int left = (a.k - (k0 + kt) * kStep) * Step::kBytes;
-    lds_char *s = (lds_char *)stage;
-    HA::load(s, view(pa, la), va, HA::past(left));
-    HA::load(s + HA::kBytes, view(pa + a_half, la - a_half), va, HA::past(left));
-    HB::load(s + 2 * HA::kBytes, view(pb, lb), vb, HB::past(left));
-    HB::load(s + 2 * HA::kBytes + HB::kBytes, view(pb + b_half, lb - b_half), vb, HB::past(left));
-  };
-  auto compute = [&](const char *stage) {
-    const lds_char *s = (const lds_char *)stage;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      i32x4 fb[TN][2];
-#pragma unroll
-      for (int y = 0; y < TN; ++y) HB::read(s + 2 * HA::kBytes + j * HB::kBytes, wn * (HN / 4), y, fb[y]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int x = 0; x < TM; ++x) {
-          i32x4 fa[2];
-          HA::read(s + i * HA::kBytes, wm * (HM / 2), x, fa);
-#pragma unroll
-          for (int y = 0; y < TN; ++y) acc[i][j][x][y] = Step::mma(fa, fb[y], acc[i][j][x][y]);
-        }
+  // half h of a's (b's) stage kt into its place; past the last stage zeros are
+  // written, so that the counts below always hold.  By row the two halves'
+  // views stay and the offset moves; by column the halves share a view, whose
+  // base moves, as the whole operand may be beyond an offset's 32 bits.
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_char *)lds;
+  const uint32_t mine = base + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / 64) * 1024;
+  const int k_end = (k0 + kn) * kStep < a.k ? kn * kStep : a.k - k0 * kStep;  // elements of this split
+  const i32x4 ra[2] = {view((const char *)a.a + a0, a.a_bytes - a0),
+                       view((const char *)a.a + a0 + a_half, a.a_bytes - a0 - a_half)};
+  const i32x4 rb[2] = {view((const char *)a.b + b0, a.b_bytes - b0),
+                       view((const char *)a.b + b0 + b_half, a.b_bytes - b0 - b_half)};
+  auto fetch_a = [&](int kt, int odd, int h) {
+    const uint32_t to = mine + odd * kStage + h * HA::kBytes;
+    if (!ACOL) {
+      HA::load(to, ra[h], va, kt * 128, HA::past((k_end - kt * kStep) * Step::kBytes));
+    } else {
+      const int64_t at = a0 + kt * a_step;
+      HA::load(to, view((const char *)a.a + at, kt < kn ? a.a_bytes - at : 0), va, h * HM * 2, 0);
     }
+  };
+  auto fetch_b = [&](int kt, int odd, int h) {
+    const uint32_t to = mine + odd * kStage + 2 * HA::kBytes + h * HB::kBytes;
+    if (!BCOL) {
+      HB::load(to, rb[h], vb, kt * 128, HB::past((k_end - kt * kStep) * Step::kBytes));
+    } else {
+      const int64_t at = b0 + kt * b_step;
+      HB::load(to, view((const char *)a.b + at, kt < kn ? a.b_bytes - at : 0), vb, h * HN * 2, 0);
+    }
+  };
+  // the second stage is beyond the 16 bits of a read's constant offset: its
+  // addresses are registers of their own (which the compiler must not know,
+  // or it makes one for every constant)
+  constexpr int NA = HA::template kAddr<TM>, NB = HB::template kAddr<TN>;
+  uint32_t pa[2][NA], pb[2][NB];
+#pragma unroll
+  for (int odd = 0; odd < 2; ++odd) {
+    HA::template addresses<TM>(base + odd * kStage, wm * (HM / 2), pa[odd]);
+    HB::template addresses<TN>(base + odd * kStage + 2 * HA::kBytes, wn * (HN / 4), pb[odd]);
+#pragma unroll
+    for (int i = 0; i < NA; ++i) asm volatile("" : "+v"(pa[odd][i]));
+#pragma unroll
+    for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(pb[odd][i]));
+  }
+  i32x4 fa[TM][2], fb[2][TN][2];
+  auto read_a = [&](int odd, int h) {
+#pragma unroll
+    for (int x = 0; x < TM; ++x) HA::template read<TM>(pa[odd], h * HA::kBytes, x, fa[x]);
+  };
+  auto read_b = [&](int odd, int h) {
+#pragma unroll
+    for (int y = 0; y < TN; ++y) HB::template read<TN>(pb[odd], h * HB::kBytes, y, fb[h][y]);
+  };
+  auto multiply = [&](int i, int j) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int x = 0; x < TM; ++x)
+#pragma unroll
+      for (int y = 0; y < TN; ++y) acc[i][j][x][y] = Step::mma(fa[x], fb[j][y], acc[i][j][x][y]);
+    __builtin_amdgcn_s_setprio(0);
   };
 
-  // A stage's loads are in flight while the other stage is worked on.  The
-  // barrier at the top of a step stands between the reads of a stage and the
-  // loads that write over it.
-  if (kn > 0) fetch(0, lds0);
-  for (int kt = 0; kt < kn; kt += 2) {
-    __syncthreads();
-    if (kt + 1 < kn) fetch(kt + 1, lds1);
-    compute(lds0);
-    if (kt + 1 < kn) {
-      __syncthreads();
-      if (kt + 2 < kn) fetch(kt + 2, lds0);
-      compute(lds1);
+  // The stages run through a pipeline of quarters.  The two waves of a SIMD
+  // (w and w + 4) take turns: in one section a wave reads the next quarter's
+  // fragments from LDS and asks for a half of a later stage, in the next it
+  // multiplies while the other wave reads; a barrier ends every section, and
+  // waves 4 .. 7 start one section late.  A stage's quarters go
+  //   (a0, b0) (a0, b1) (a1, b1) (a1, b0)   in even stages,
+  //   (a0, b1) (a0, b0) (a1, b0) (a1, b1)   in odd ones,
+  // so each quarter but the last brings in one new half, and the last, which
+  // brings none, reads the b half that the next stage begins with.  A half's
+  // place is free once both waves have read it (their reads have arrived
+  // before the barrier), so the same half of two stages on is asked for one
+  // quarter later and has six quarters to arrive: kAhead loads are younger
+  // than the ones that the next quarter reads.
+  constexpr int kAhead = 3 * (HA::kLoads + HB::kLoads);
+  auto quarter = [&](auto read, auto fetch, int i, int j) {
+    read();
+    fetch();
+    arrived<kAhead>();
+    meet();
+    multiply(i, j);
+    meet();
+  };
+  if (kn > 0) {
+    fetch_b(0, 0, 0), fetch_a(0, 0, 0), fetch_b(0, 0, 1), fetch_a(0, 0, 1);
+    fetch_b(1, 1, 1), fetch_a(1, 1, 0), fetch_b(1, 1, 0), fetch_a(1, 1, 1);
+    arrived<kAhead>();
+    meet();
+    read_b(0, 0);
+    arrived<kAhead>();
+    meet();
+    if (wm) meet();
+    for (int kt = 0; kt < kn; kt += 2) {
+      quarter([&] { read_a(0, 0); }, [&] { fetch_b(kt + 2, 0, 0); }, 0, 0);
+      quarter([&] { read_b(0, 1); }, [&] { fetch_a(kt + 2, 0, 0); }, 0, 1);
+      quarter([&] { read_a(0, 1); }, [&] { fetch_b(kt + 2, 0, 1); }, 1, 1);
+      quarter([&] { read_b(1, 1); }, [&] { fetch_a(kt + 2, 0, 1); }, 1, 0);
+      // an odd number of stages: the last is all zeros and adds nothing
+      quarter([&] { read_a(1, 0); }, [&] { fetch_b(kt + 3, 1, 1); }, 0, 1);
+      quarter([&] { read_b(1, 0); }, [&] { fetch_a(kt + 3, 1, 0); }, 0, 0);
+      quarter([&] { read_a(1, 1); }, [&] { fetch_b(kt + 3, 1, 0); }, 1, 0);
+      quarter([&] { read_b(0, 0); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 1);
     }
+    if (!wm) meet();
+    // nothing may still be on its way to LDS when its bytes are used again
+    arrived<0>();
   }
 
   // Out: the sums of HM rows at a time go through LDS, so that a thread has 8
@@ -258,10 +367,12 @@ template <class Step, bool ACOL, bool BCOL>
 hipError_t go(const ProductArgs &a, hipStream_t s) {
   const int64_t tile = a.tile == 0 ? 256 : 128, tile_n = a.e.gated ? tile / 2 : tile;
   const dim3 grid((unsigned)(((a.m + tile - 1) / tile) * ((a.n + tile_n - 1) / tile_n)), (unsigned)a.splits);
-  if (a.tile == 0)
-    product_kernel<Step, ACOL, BCOL, 128, 128><<<grid, 512, 0, s>>>(a);
-  else
+  if (a.tile == 0) {
+    if constexpr (Step::kWide) return hipErrorInvalidValue;  // never planned
+    else product_kernel<Step, ACOL, BCOL, 128, 128><<<grid, 512, 0, s>>>(a);
+  } else {
     product_kernel<Step, ACOL, BCOL, 64, 64><<<grid, 512, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -100,6 +100,7 @@ __device__ __forceinline__ void finish(const Epilogue &e, int m, int n, float (&
 // holds is the same for a and b, and their order does not matter to a sum.
 struct StepBF16 {
   typedef f32x4 Acc;
+  static constexpr bool kWide = false;
   static constexpr int kBytes = 2;
   static __device__ __forceinline__ Acc mma(const i32x4 (&a)[2], const i32x4 (&b)[2], Acc c) {
 #pragma unroll
@@ -112,6 +113,7 @@ struct StepBF16 {
 };
 struct StepF16 {
   typedef f32x4 Acc;
+  static constexpr bool kWide = false;
   static constexpr int kBytes = 2;
   static __device__ __forceinline__ Acc mma(const i32x4 (&a)[2], const i32x4 (&b)[2], Acc c) {
 #pragma unroll
@@ -126,6 +128,7 @@ struct StepF16 {
 // through the f16 instructions at half the f8 rate.
 struct StepF8Wide {
   typedef f32x4 Acc;
+  static constexpr bool kWide = true;
   static constexpr int kBytes = 1;
   static __device__ __forceinline__ f16x8 widen(int lo, int hi) {
     typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -153,6 +156,7 @@ struct StepF8Wide {
 // results and contractions of one step take StepF8Wide.
 struct StepF8 {
   typedef f32x4 Acc;
+  static constexpr bool kWide = false;
   static constexpr int kBytes = 1;
   static __device__ __forceinline__ Acc mma(const i32x4 (&a)[2], const i32x4 (&b)[2], Acc c) {
     const i32x8 x = __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7);
@@ -161,11 +165,10 @@ struct StepF8 {
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
 };
-constexpr bool f8_wide(int out_dtype, int k) { return out_dtype == HF_F32 || k <= 128; }
-
 // s8: sums in 32-bit integers, exact up to contractions of 2^17
 struct StepS8 {
   typedef i32x4 Acc;
+  static constexpr bool kWide = false;
   static constexpr int kBytes = 1;
   static __device__ __forceinline__ Acc mma(const i32x4 (&a)[2], const i32x4 (&b)[2], Acc c) {
 #pragma unroll
