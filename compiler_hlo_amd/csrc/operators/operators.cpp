@@ -147,21 +147,31 @@ void choose(hf_operator &op, Product &p, int64_t elem) {
   const int64_t kbytes = p.k * elem;
   p.ldp = p.gated ? 2 * up(p.n, 8) : up(p.n, 8);
   p.splits = 1;
-  if (!p.a_by_col && !p.b_by_col && p.m <= 64) {
+  // e4m3 widened to 16 bits has no registers to spare for the larger tile or
+  // for 16 waves a workgroup
+  const bool wide = op.d.dtype == HF_F8E4M3 && f8_wide(op.d.out_dtype, p.k);
+  if (!p.a_by_col && !p.b_by_col && p.m <= 8) {
     p.skinny = true;
     const int64_t columns = cdiv(p.n, 16), blocks = cdiv(kbytes, 512);
-    // 16 waves a workgroup where there are too few workgroups to fill the
-    // chip with 8
-    p.waves = columns <= 512 && p.m <= 32 ? 16 : 8;
+    // As many waves a workgroup as let all workgroups run at once (about 5000
+    // waves fit): a second round of workgroups for the last few costs as much
+    // as the first.
+    p.waves = columns * 16 <= 5120 && !wide ? 16 : columns * 8 <= 5120 ? 8 : 4;
     int64_t s = 1;
     while (columns * s < 256 && blocks >= 2 * s * p.waves) s *= 2;
     p.per_split = (int)cdiv(blocks > 0 ? blocks : 1, s);
     p.splits = blocks > 0 ? (int)cdiv(blocks, p.per_split) : 1;
+  } else if (!p.a_by_col && !p.b_by_col && p.m <= 64) {
+    p.tile = 2;
+    const int64_t strips = cdiv(p.n, p.gated ? 128 : 256), steps = cdiv(p.k, 128 / elem);
+    // one workgroup a compute unit, with at least 4 stages of the contraction
+    int64_t s = strips < 256 ? 256 / strips : 1;
+    if (s > steps / 4) s = steps / 4 > 0 ? steps / 4 : 1;
+    p.per_split = (int)cdiv(steps > 0 ? steps : 1, s);
+    p.splits = steps > 0 ? (int)cdiv(steps, p.per_split) : 1;
   } else {
     const int64_t steps = cdiv(p.k, 128 / elem);
     auto tiles = [&](int64_t t) { return cdiv(p.m, t) * cdiv(p.n, p.gated ? t / 2 : t); };
-    // e4m3 widened to 16 bits has no registers to spare for the larger tile
-    const bool wide = op.d.dtype == HF_F8E4M3 && f8_wide(op.d.out_dtype, p.k);
     p.tile = tiles(256) >= 192 && !wide ? 0 : 1;
     int64_t s = 1;
     if (p.tile == 1)
@@ -381,8 +391,8 @@ void make_plan(hf_operator &op) {
     const int64_t wide = d.kind == HF_OPERATOR_GATED || d.kind == HF_OPERATOR_GATED_GRAD ? 2 * d.n : d.n;
     f.algorithmic_flops = (grad ? 4 : 2) * d.m * wide * d.k;
     if (op.p1.on) {
-      f.tile_rows = op.p1.skinny ? 16 * (op.p1.m <= 16 ? 1 : op.p1.m <= 32 ? 2 : 4) : op.p1.tile == 0 ? 256 : 128;
-      f.tile_cols = op.p1.skinny ? (op.p1.gated ? 32 : 16) : f.tile_rows;
+      f.tile_rows = op.p1.skinny ? 16 : op.p1.tile == 0 ? 256 : op.p1.tile == 1 ? 128 : 64;
+      f.tile_cols = op.p1.skinny ? (op.p1.gated ? 32 : 16) : op.p1.tile == 1 ? 128 : 256;
       f.splits = op.p1.splits;
     }
   }

@@ -95,7 +95,7 @@ struct ProductArgs {
   int32_t m, n, k;           // n: columns of d (gated: of one half); k: elements
   int32_t dtype;
   bool a_by_col, b_by_col;   // the contraction runs over the operand's rows
-  int32_t tile;              // 0: 256 x 256, 1: 128 x 128 (columns of the product)
+  int32_t tile;              // 0: 256 x 256, 1: 128 x 128 (columns of the product), 2: strips, m <= 64 by row
   int32_t splits, k_tiles_per_split;
   float *partial;            // [splits][m][ldp] when splits > 1
   int64_t ldp;
@@ -107,7 +107,7 @@ constexpr bool f8_wide(int out_dtype, int64_t k) { return out_dtype == HF_F32 ||
 
 struct SkinnyArgs {
   ProductArgs p;             // splits: workgroups over k
-  int32_t waves;             // 8 or 16
+  int32_t waves;             // of a workgroup: 4, 8 or 16
   int32_t blocks_per_split;  // blocks of 512 contraction bytes
 };
 hipError_t launch_skinny(const SkinnyArgs &a, hipStream_t s);

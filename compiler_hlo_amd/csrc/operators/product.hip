@@ -52,22 +52,31 @@ __device__ __forceinline__ void meet() {
 // One half (R rows of the operand's tile, 128 bytes of the contraction) of a
 // stage in LDS, and how it gets there.
 //
+// LDS has 64 banks of 4 bytes, and 16 lanes of a 16-byte read (32 of an 8-byte
+// one) go at once.
+//
 // By row (the contraction lies along the operand's rows): LDS row r holds the
-// 8 16-byte chunks of tile row r, chunk c at slot c ^ (r % 8), so that the 8
-// lanes that read one chunk of 8 rows meet 8 different slots.
+// 8 16-byte chunks of tile row r, chunk c at slot c ^ (r / 2 % 8).  Two rows
+// fill the banks, and the lanes of one turn (rows 0-3 and 12-15 of one chunk,
+// 4-11 of the next, or the others) meet 8 different slots in each of the two.
 // By column (the contraction runs over the operand's rows; 16-bit types):
 // LDS row k holds R columns of contraction step k in units of 16 columns (32
-// bytes), unit u at u ^ f(k) with f(k) = k % 4 + 4 (k / 8 % 2) (R = 64:
-// k % 4), so that the 16 lanes that read 4 steps of one unit, and the next 16
-// lanes 8 steps on, meet different banks; ds_read_b64_tr_b16 turns the unit.
+// bytes), unit u at u ^ f(k).  The lanes of one turn read steps k .. k + 3 and
+// k + 8 .. k + 11 of one unit, and f tells those apart: 3 bits of k where a
+// row fills the banks, 2 where two rows do.  ds_read_b64_tr_b16 turns the
+// unit.
 //
 // The loads write LDS directly, 1 KiB a wave: lane l of a wave fills bytes
 // 16 l .. of its kilobyte, so the swizzle is in which global bytes it asks
 // for.
-template <int R, bool COL>
+template <int R, bool COL, int WAVES>
 struct Half {
   static constexpr int kBytes = R * 128;
-  static constexpr int kLoads = kBytes / 8192;  // 16-byte loads a thread
+  static constexpr int kLoads = kBytes / (WAVES * 1024);  // 16-byte loads a thread
+
+  static __device__ __forceinline__ int f(int k) {
+    return R == 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+  }
 
   // The global offsets of this thread's loads, from the tile's first row (by
   // row) or first column (by column) at the stage's first contraction byte.
@@ -75,72 +84,77 @@ struct Half {
     const int w = threadIdx.x / 64, l = threadIdx.x % 64;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int piece = w + 8 * i;
+      const int piece = w + WAVES * i;
       if (!COL) {
         const int row = piece * 8 + l / 8;
-        v[i] = (uint32_t)(row * ld) + (uint32_t)(((l & 7) ^ (l >> 3)) * 16);
+        v[i] = (uint32_t)(row * ld) + (uint32_t)(chunk() * 16);
       } else {
         constexpr int per = R * 2 / 16;  // lanes a step
         const int k = piece * (64 / per) + l / per, slot = l % per;
-        const int f = (k & 3) | (R == 128 ? ((k >> 3) & 1) << 2 : 0);
-        v[i] = (uint32_t)(k * ld) + (uint32_t)((((slot >> 1) ^ f) * 32) + (slot & 1) * 16);
+        v[i] = (uint32_t)(k * ld) + (uint32_t)((((slot >> 1) ^ f(k)) * 32) + (slot & 1) * 16);
       }
     }
   }
-  // by row: set where this thread's chunk lies past `left` contraction bytes
-  static __device__ __forceinline__ uint32_t past(int left) {
-    const int l = threadIdx.x % 64;
-    return !COL && ((l & 7) ^ (l >> 3)) * 16 >= left ? 0x80000000u : 0u;
+  // by row: the chunk that this thread loads, the same in all its pieces (as
+  // WAVES is even), and whether it lies past `left` contraction bytes
+  static __device__ __forceinline__ int chunk() {
+    const int l = threadIdx.x % 64, w = threadIdx.x / 64;
+    return (l & 7) ^ ((w & 1) * 4 + (l >> 4));
   }
+  static __device__ __forceinline__ uint32_t past(int left) { return !COL && chunk() * 16 >= left ? 0x80000000u : 0u; }
   // into LDS from `lds` on (this wave's first kilobyte)
   static __device__ __forceinline__ void load(uint32_t lds, i32x4 r, const uint32_t (&v)[kLoads], uint32_t at,
                                               uint32_t past) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_to_lds(lds + i * 8192, r, COL ? v[i] : v[i] | past, at);
+    for (int i = 0; i < kLoads; ++i) load_to_lds(lds + i * (WAVES * 1024), r, COL ? v[i] : v[i] | past, at);
   }
 
-  // This lane's LDS addresses for the fragments of T tiles from row (column)
-  // `base` of the half on: one for each half of the contraction bytes by row,
-  // one for each tile by column.  Everything else is a constant.
+  // This lane's LDS addresses for the fragments of T tiles of 16 rows
+  // (columns) from row `base` of the half on: by row one for each half of the
+  // contraction bytes, by column one for each tile.  Everything else is a
+  // constant.
   template <int T>
   static constexpr int kAddr = COL ? T : 2;
   template <int T>
   static __device__ __forceinline__ void addresses(uint32_t lds, int base, uint32_t (&p)[kAddr<T>]) {
     const int l = threadIdx.x % 64, g = l >> 4, i = l & 15;
-    const int s = (i >> 2) | (R == 128 ? (g & 1) << 2 : 0);
 #pragma unroll
     for (int t = 0; t < kAddr<T>; ++t) {
-      p[t] = lds + (COL ? (g * 8 + (i >> 2)) * (R * 2) + (((base / 16 + t) ^ s) * 32) + (i & 3) * 8
-                        : (base + i) * 128 + ((g ^ (l & 7) ^ (t * 4)) * 16));
+      const int k = g * 8 + (i >> 2);
+      p[t] = lds + (COL ? k * (R * 2) + (((base / 16 + t) ^ f(k)) * 32) + (i & 3) * 8
+                        : (base + i) * 128 + (((4 * t + g) ^ (i >> 1)) * 16));
     }
   }
-  // The fragment of tile t: rows (columns) base + 16 t + l % 16.
+  // The fragment of tile t, rows (columns) base + 16 t + l % 16: piece h holds
+  // this lane's 16 of the 64 bytes h of the contraction's 128.
   template <int T>
-  static __device__ __forceinline__ void read(const uint32_t (&p)[kAddr<T>], uint32_t at, int t, i32x4 (&f)[2]) {
+  static __device__ __forceinline__ void read(const uint32_t (&p)[kAddr<T>], uint32_t at, int t, i32x4 (&v)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (!COL) {
-        f[h] = *(const __attribute__((address_space(3))) i32x4 *)(p[h] + at + t * 2048);
+        v[h] = *(const __attribute__((address_space(3))) i32x4 *)(uintptr_t)(p[h] + at + t * 2048);
       } else {
         typedef __attribute__((address_space(3))) i16x4 tr;
-        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(p[t % kAddr<T>] + at + h * (R * 64)));
-        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(p[t % kAddr<T>] + at + h * (R * 64) + R * 8));
-        f[h] = __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        const uint32_t q = p[t % kAddr<T>] + at + h * (R * 64);
+        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(uintptr_t)q);
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr *)(uintptr_t)(q + R * 8));
+        v[h] = __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
     }
   }
 };
 
-// A workgroup of 8 waves computes 2 HM x 2 HN sums (HM = HN = 128: 256 x 256;
-// 64: 128 x 128), 128 contraction bytes a stage, two stages in LDS.  A wave
-// has, in each quarter of the tile, HM/2 x HN/4 sums; gated, the second half
-// of the columns is the up half of the first, so a lane holds gate and up of
-// the same element.
+// A workgroup computes 2 HM x 2 HN sums, 128 contraction bytes a stage, two
+// stages in LDS: 256 x 256 with 8 waves, one workgroup a compute unit, or
+// 128 x 128 with 4 waves, two of them.  A wave has HM/2 x 32 sums in each
+// quarter of the tile; gated, the second half of the columns is the up half
+// of the first, so a lane holds gate and up of the same element.
 template <class Step, bool ACOL, bool BCOL, int HM, int HN>
-__global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(ProductArgs a) {
-  typedef Half<HM, ACOL> HA;
-  typedef Half<HN, BCOL> HB;
-  constexpr int TM = HM / 32, TN = HN / 64;  // 16 x 16 tiles of a wave in a quarter
+__global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void product_kernel(ProductArgs a) {
+  constexpr int WN = HN / 32, WAVES = 2 * WN, THREADS = WAVES * 64;
+  typedef Half<HM, ACOL, WAVES> HA;
+  typedef Half<HN, BCOL, WAVES> HB;
+  constexpr int TM = HM / 32, TN = 2;  // 16 x 16 tiles of a wave in a quarter
   constexpr int kStage = 2 * HA::kBytes + 2 * HB::kBytes;
   // the stages, then rows of 2 HN sums with a pad of 16 bytes (Out)
   constexpr int kPitch = 2 * HN + 4;
@@ -165,7 +179,7 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
   const int tm = first + (id - group * G * tiles_n) % size, tn = (id - group * G * tiles_n) / size;
   const int m0 = tm * 2 * HM, n0 = tn * tile_n;
 
-  const int w = threadIdx.x / 64, wm = w / 4, wn = w % 4;
+  const int w = threadIdx.x / 64, wm = w / WN, wn = w % WN;
   const int k0 = blockIdx.y * a.k_tiles_per_split;
   constexpr int kStep = 128 / Step::kBytes;  // elements of the contraction a stage
   const int all = (a.k + kStep - 1) / kStep;
@@ -230,7 +244,7 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
 #pragma unroll
   for (int odd = 0; odd < 2; ++odd) {
     HA::template addresses<TM>(base + odd * kStage, wm * (HM / 2), pa[odd]);
-    HB::template addresses<TN>(base + odd * kStage + 2 * HA::kBytes, wn * (HN / 4), pb[odd]);
+    HB::template addresses<TN>(base + odd * kStage + 2 * HA::kBytes, wn * 32, pb[odd]);
 #pragma unroll
     for (int i = 0; i < NA; ++i) asm volatile("" : "+v"(pa[odd][i]));
 #pragma unroll
@@ -248,9 +262,11 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
   auto multiply = [&](int i, int j) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int x = 0; x < TM; ++x)
+    for (int k = 0; k < Step::kSteps; ++k)
 #pragma unroll
-      for (int y = 0; y < TN; ++y) acc[i][j][x][y] = Step::mma(fa[x], fb[j][y], acc[i][j][x][y]);
+      for (int y = 0; y < TN; ++y)
+#pragma unroll
+        for (int x = 0; x < TM; ++x) acc[i][j][x][y] = Step::step(fa[x], fb[j][y], acc[i][j][x][y], k);
     __builtin_amdgcn_s_setprio(0);
   };
 
@@ -258,7 +274,9 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
   // (w and w + 4) take turns: in one section a wave reads the next quarter's
   // fragments from LDS and asks for a half of a later stage, in the next it
   // multiplies while the other wave reads; a barrier ends every section, and
-  // waves 4 .. 7 start one section late.  A stage's quarters go
+  // waves 4 .. 7 start one section late.  (With 4 waves the other wave of a
+  // SIMD is another workgroup's, and the two fall into step by themselves.)  A
+  // stage's quarters go
   //   (a0, b0) (a0, b1) (a1, b1) (a1, b0)   in even stages,
   //   (a0, b1) (a0, b0) (a1, b0) (a1, b1)   in odd ones,
   // so each quarter but the last brings in one new half, and the last, which
@@ -284,7 +302,7 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
     read_b(0, 0);
     arrived<kAhead>();
     meet();
-    if (wm) meet();
+    if (WAVES == 8 && wm) meet();
     for (int kt = 0; kt < kn; kt += 2) {
       quarter([&] { read_a(0, 0); }, [&] { fetch_b(kt + 2, 0, 0); }, 0, 0);
       quarter([&] { read_b(0, 1); }, [&] { fetch_a(kt + 2, 0, 0); }, 0, 1);
@@ -296,15 +314,14 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
       quarter([&] { read_a(1, 1); }, [&] { fetch_b(kt + 3, 1, 0); }, 1, 0);
       quarter([&] { read_b(0, 0); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 1);
     }
-    if (!wm) meet();
+    if (WAVES == 8 && !wm) meet();
     // nothing may still be on its way to LDS when its bytes are used again
     arrived<0>();
   }
 
   // Out: the sums of HM rows at a time go through LDS, so that a thread has 8
   // consecutive columns of a row and a row's stores are contiguous.  A lane's
-  // four sums are 16 bytes; the pad keeps the 16 rows of a tile in different
-  // banks.
+  // four sums are 16 bytes; the pad keeps neighbouring rows in different banks.
   const int l = threadIdx.x % 64;
   float *out = (float *)lds;
   const int per = tile_n / 8;  // threads a row
@@ -317,11 +334,11 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int y = 0; y < TN; ++y)
-          *(f32x4 *)(out + (wm * (HM / 2) + x * 16 + (l & 15)) * kPitch + j * HN + wn * (HN / 4) + y * 16 +
-                     (l >> 4) * 4) = Step::sums(acc[i][j][x][y]);
+          *(f32x4 *)(out + (wm * (HM / 2) + x * 16 + (l & 15)) * kPitch + j * HN + wn * 32 + y * 16 + (l >> 4) * 4) =
+              Step::sums(acc[i][j][x][y]);
     __syncthreads();
 #pragma unroll 1
-    for (int at = threadIdx.x; at < HM * per; at += 512) {
+    for (int at = threadIdx.x; at < HM * per; at += THREADS) {
       const int r = at / per, c = at % per * 8, m = m0 + i * HM + r, n = n0 + c;
       float v[8], u[8];
       load8<F32>(out + r * kPitch + c, v);
@@ -336,6 +353,121 @@ __global__ __launch_bounds__(512, HM == 128 ? 2 : 4) void product_kernel(Product
       } else {
         finish<8>(a.e, m, n, v, u);
       }
+    }
+  }
+}
+
+// The product for up to 64 rows, bound by reading b: a strip of 256 columns
+// (gated: 128 and their up half) a workgroup of 8 waves, 16 columns of each
+// half a wave, all rows.  Both operands go through LDS in whole 128-byte
+// lines, a once for 256 columns.  Three stages of 40 KiB, two of them in
+// flight: more than the memory's latency times its rate a compute unit needs.
+template <class Step>
+__global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
+  typedef Half<64, false, 8> HA;
+  typedef Half<128, false, 8> HB;
+  constexpr int TM = 4;
+  constexpr int kStage = HA::kBytes + 2 * HB::kBytes, kStages = 3;
+  constexpr int kPitch = 256 + 4;
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+  static_assert(64 * kPitch * 4 <= kStages * kStage, "the sums go out through the stages");
+
+  const bool gated = a.e.gated;
+  const int width = gated ? 128 : 256;
+  const int n0 = blockIdx.x * width;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
+  constexpr int kStep = 128 / Step::kBytes;
+  const int k0 = blockIdx.y * a.k_tiles_per_split;
+  const int all = (a.k + kStep - 1) / kStep;
+  const int kn = all - k0 < a.k_tiles_per_split ? all - k0 : a.k_tiles_per_split;
+  const int left = (k0 + kn) * kStep < a.k ? kn * 128 : (a.k - k0 * kStep) * Step::kBytes;
+  const int64_t a0 = (int64_t)k0 * 128, b0 = (int64_t)n0 * a.ldb + (int64_t)k0 * 128;
+  const int64_t b_half = gated ? a.b_half : 128 * a.ldb;
+  const i32x4 ra = view((const char *)a.a + a0, a.a_bytes - a0);
+  const i32x4 rb[2] = {view((const char *)a.b + b0, a.b_bytes - b0),
+                       view((const char *)a.b + b0 + b_half, a.b_bytes - b0 - b_half)};
+  uint32_t va[HA::kLoads], vb[HB::kLoads];
+  HA::offsets(a.lda, va);
+  HB::offsets(a.ldb, vb);
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_char *)lds;
+  // Workgroups begin at stages of their own and go round, so that rows a
+  // power of two apart do not keep all of them on the same memory channels.
+  const int turn = kn > 0 ? (int)((blockIdx.x * 7u + blockIdx.y) % (uint32_t)kn) : 0;
+  auto fetch = [&](int kt, int stage) {
+    int t = kt + turn;
+    t = t >= kn ? t - kn : t;
+    const uint32_t past = kt < kn ? HA::past(left - t * 128) : 0x80000000u;
+    const uint32_t to = base + stage * kStage + w * 1024;
+    HA::load(to, ra, va, t * 128, past);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) HB::load(to + HA::kBytes + h * HB::kBytes, rb[h], vb, t * 128, past);
+  };
+  typename Step::Acc acc[2][TM];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int x = 0; x < TM; ++x) acc[j][x] = typename Step::Acc{0, 0, 0, 0};
+  uint32_t pa[2], pb[2];
+  HA::addresses<TM>(base, 0, pa);
+  HB::addresses<1>(base + HA::kBytes, w * 16, pb);
+  auto add = [&](int stage) {
+    const uint32_t at = stage * kStage;
+    i32x4 fb[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) HB::read<1>(pb, at + j * HB::kBytes, 0, fb[j]);
+#pragma unroll
+    for (int x = 0; x < TM; ++x) {
+      if (x * 16 >= a.m) break;
+      i32x4 fa[2];
+      HA::read<TM>(pa, at, x, fa);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[j][x] = mma<Step>(fa, fb[j], acc[j][x]);
+    }
+  };
+  // A stage's loads have arrived when only the next stage's are left; after
+  // the barrier every wave's have, and every wave is done with the stage
+  // before it, whose place the stage after the next then takes.
+  constexpr int kLoads = HA::kLoads + 2 * HB::kLoads;
+  if (kn > 0) {
+    fetch(0, 0);
+    fetch(1, 1);
+    for (int kt = 0; kt < kn; kt += 3) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        arrived<kLoads>();
+        meet();
+        if (kt + i < kn) {
+          fetch(kt + i + 2, (i + 2) % 3);
+          add(i);
+        } else {
+          fetch(kn, (i + 2) % 3);
+        }
+      }
+    }
+    arrived<0>();
+  }
+  float *out = (float *)lds;
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < TM; ++x)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *(f32x4 *)(out + (x * 16 + (l & 15)) * kPitch + j * 128 + w * 16 + (l >> 4) * 4) = Step::sums(acc[j][x]);
+  __syncthreads();
+  const int per = width / 8;
+#pragma unroll 1
+  for (int at = threadIdx.x; at < a.m * per; at += 512) {
+    const int m = at / per, c = at % per * 8, n = n0 + c;
+    if (n >= a.n) continue;
+    float v[8], u[8];
+    load8<F32>(out + m * kPitch + c, v);
+    if (gated) load8<F32>(out + m * kPitch + 128 + c, u);
+    if (a.splits > 1) {
+      float *p = a.partial + ((int64_t)blockIdx.y * a.m + m) * a.ldp + n;
+      store8<F32>(p, v);
+      if (gated) store8<F32>(p + a.ldp / 2, u);
+    } else {
+      finish<8>(a.e, m, n, v, u);
     }
   }
 }
@@ -371,13 +503,21 @@ hipError_t go(const ProductArgs &a, hipStream_t s) {
     if constexpr (Step::kWide) return hipErrorInvalidValue;  // never planned
     else product_kernel<Step, ACOL, BCOL, 128, 128><<<grid, 512, 0, s>>>(a);
   } else {
-    product_kernel<Step, ACOL, BCOL, 64, 64><<<grid, 512, 0, s>>>(a);
+    product_kernel<Step, ACOL, BCOL, 64, 64><<<grid, 256, 0, s>>>(a);
   }
   return hipGetLastError();
 }
 
 template <class Step>
+hipError_t go_strip(const ProductArgs &a, hipStream_t s) {
+  const int width = a.e.gated ? 128 : 256;
+  strip_kernel<Step><<<dim3((unsigned)((a.n + width - 1) / width), (unsigned)a.splits), 512, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class Step>
 hipError_t by_layout(const ProductArgs &a, hipStream_t s) {
+  if (a.tile == 2) return go_strip<Step>(a, s);
   if (!a.a_by_col && !a.b_by_col) return go<Step, false, false>(a, s);
   if constexpr (Step::kBytes == 2) {
     if (!a.a_by_col) return go<Step, false, true>(a, s);

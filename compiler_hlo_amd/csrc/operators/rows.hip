@@ -49,6 +49,35 @@ __device__ __forceinline__ void store_row(typename E::Store *row, int t, int j, 
   }
 }
 
+// The same in two parts: the bits as they come from memory, asked for a row
+// ahead, and their values.
+template <class E, int T, bool VEC>
+struct Raw {
+  u32x4 v[E::kBytes / 2];        // VEC
+  typename E::Store one[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const typename E::Store *row, int t, int j, int cols) {
+    if (VEC) {
+      const int c = column<T, VEC>(t, j, 0);
+#pragma unroll
+      for (int i = 0; i < E::kBytes / 2; ++i) v[i] = c < cols ? ((const u32x4 *)(row + c))[i] : u32x4{0, 0, 0, 0};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = column<T, VEC>(t, j, i);
+        one[VEC ? 0 : i] = c < cols ? row[c] : (typename E::Store)0;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!VEC) f[i] = E::load(one[VEC ? 0 : i]);
+      else if (E::kBytes == 4) f[i] = __uint_as_float(v[i / 4 % (E::kBytes / 2)][i % 4]);
+      else f[i] = E::load((typename E::Store)(uint16_t)(v[0][i / 2] >> (i % 2 * 16)));
+    }
+  }
+};
+
 // The weight, in f32 or in the rows' type.
 template <class E, int T, bool VEC>
 __device__ __forceinline__ void load_weight(const void *w, bool wide, int t, int j, int cols, float (&v)[8]) {
@@ -322,11 +351,12 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a) {
 
 // RmsNormGrad.  With xh = h rstd and g = dy weight,
 //   dx = (g - xh mean(g xh)) rstd + dstream,   dweight = sum over rows dy xh.
-// A workgroup (one wave in rows of 1024 or fewer) takes every groups-th row
+// A workgroup (one wave in rows of 512 or fewer) takes every groups-th row
 // and keeps its columns' dweight in registers over all of them, so dweight
 // costs no memory traffic but one partial row a group; fold_kernel adds the
 // groups in a fixed order.  Bound by memory: dy, h and dstream read once, dx
-// written once.
+// written once.  A row's mean stands between its loads and its stores, so the
+// next row is asked for before that.
 template <class E, int T, int NV, bool VEC>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_grad_kernel(NormGradArgs a) {
   __shared__ float slots[2][T == 64 ? 1 : T / 64];
@@ -335,108 +365,136 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_grad_kernel(NormGradAr
   const int group = blockIdx.x * PER + threadIdx.x / T;
   if (group >= a.groups) return;
   typedef typename E::Store S;
-  const bool wide = a.weight_dtype == HF_F32;
-  const int n = NV ? NV : (a.cols + 8 * T - 1) / (8 * T);
-  constexpr int K = NV ? NV : 1;
+  const bool wide = a.weight_dtype == HF_F32, stream = a.dstream != nullptr;
   float *partial = a.partial + (int64_t)group * a.cols;
-  float dw[K][8], w[K][8];
-  if (NV) {
+  float dw[NV][8], w[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+  }
+  Raw<E, T, VEC> rh[NV], rg[NV], rs[NV];
+  float next_rstd = 0.f;
+  auto ask = [&](int64_t row) {
+    next_rstd = a.rstd[row];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) rh[j].load((const S *)a.h + row * a.ldh, t, j, a.cols);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) rg[j].load((const S *)a.dy + row * a.lddy, t, j, a.cols);
+    if (stream) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) rs[j].load((const S *)a.dstream + row * a.ldds, t, j, a.cols);
+    }
+  };
+  if (group < a.rows) ask(group);
+  int turn = 0;
+  for (int64_t row = group; row < a.rows; row += a.groups, turn ^= 1) {
+    const float rstd = next_rstd;
+    float xh[NV][8], g[NV][8], o[NV][8];
+    float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w[j]);
+      rh[j].values(xh[j]);
+      rg[j].values(g[j]);
+      if (stream) rs[j].values(o[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        xh[j][i] *= rstd;
+        dw[j][i] = __builtin_fmaf(g[j][i], xh[j][i], dw[j][i]);
+        g[j][i] *= w[j][i];
+        dot = __builtin_fmaf(g[j][i], xh[j][i], dot);
+      }
     }
-  } else {
-    for (int j = 0; j < n; ++j) {
-      float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      store_row<F32, T, VEC>(partial, t, j, a.cols, z);
+    if (row + a.groups < a.rows) ask(row + a.groups);
+    // the slots change with each row: a thread may be one row ahead of
+    // another, never two, as each row has a barrier
+    const float mean = row_sum<T>(dot, slots[turn]) / (float)a.cols;
+    S *dx = (S *)a.dx + row * a.lddx;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[j][i] = (g[j][i] - xh[j][i] * mean) * rstd;
+        if (stream) g[j][i] += o[j][i];
+      }
+      store_row<E, T, VEC>(dx, t, j, a.cols, g[j]);
     }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) store_row<F32, T, VEC>(partial, t, j, a.cols, dw[j]);
+}
+
+// The same for rows that do not fit the registers: each is read twice, and
+// dweight's partial row is kept in memory (it is this workgroup's alone).
+template <class E, bool VEC>
+__global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
+  constexpr int T = 1024;
+  __shared__ float slots[2][T / 64];
+  const int t = threadIdx.x, group = blockIdx.x;
+  typedef typename E::Store S;
+  const bool wide = a.weight_dtype == HF_F32;
+  const int n = (a.cols + 8 * T - 1) / (8 * T);
+  float *partial = a.partial + (int64_t)group * a.cols;
+  for (int j = 0; j < n; ++j) {
+    const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    store_row<F32, T, VEC>(partial, t, j, a.cols, z);
   }
   int turn = 0;
   for (int64_t row = group; row < a.rows; row += a.groups, turn ^= 1) {
     const S *dy = (const S *)a.dy + row * a.lddy, *h = (const S *)a.h + row * a.ldh;
-    const S *ds = a.dstream ? (const S *)a.dstream + row * a.ldds : nullptr;
-    S *dx = (S *)a.dx + row * a.lddx;
     const float rstd = a.rstd[row];
-    float xh[K][8], g[K][8], o[K][8];
-    float dot = 0.f;
-    auto take = [&](int j, int k) {
-      load_row<E, T, VEC>(h, t, j, a.cols, xh[k]);
-      load_row<E, T, VEC>(dy, t, j, a.cols, g[k]);
-      if (!NV) load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w[k]);
+    float xh[8], g[8], w[8], o[8], dot = 0.f;
+    auto take = [&](int j) {
+      load_row<E, T, VEC>(h, t, j, a.cols, xh);
+      load_row<E, T, VEC>(dy, t, j, a.cols, g);
+      load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xh[i] *= rstd;
     };
-    auto join = [&](int k, bool grad) {
+    for (int j = 0; j < n; ++j) {
+      take(j);
+      load_row<F32, T, VEC>(partial, t, j, a.cols, o);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        xh[k][i] *= rstd;
-        if (grad) dw[k][i] = __builtin_fmaf(g[k][i], xh[k][i], dw[k][i]);
-        g[k][i] *= w[k][i];
-        dot = __builtin_fmaf(g[k][i], xh[k][i], dot);
+        o[i] = __builtin_fmaf(g[i], xh[i], o[i]);
+        dot = __builtin_fmaf(g[i] * w[i], xh[i], dot);
       }
-    };
-    auto put = [&](int j, int k, float mean) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[k][i] = (g[k][i] - xh[k][i] * mean) * rstd;
-        if (ds) g[k][i] += o[k][i];
-      }
-      store_row<E, T, VEC>(dx, t, j, a.cols, g[k]);
-    };
-    if (NV) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) take(j, j);
-      if (ds) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) load_row<E, T, VEC>(ds, t, j, a.cols, o[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < NV; ++j) join(j, true);
-    } else {
-      for (int j = 0; j < n; ++j) {
-        take(j, 0);
-        load_row<F32, T, VEC>(partial, t, j, a.cols, dw[0]);
-        join(0, true);
-        store_row<F32, T, VEC>(partial, t, j, a.cols, dw[0]);
-      }
+      store_row<F32, T, VEC>(partial, t, j, a.cols, o);
     }
-    // the slots change with each row: a thread may be one row ahead of
-    // another, never two, as each row has a barrier
     const float mean = row_sum<T>(dot, slots[turn]) / (float)a.cols;
-    if (NV) {
+    for (int j = 0; j < n; ++j) {
+      take(j);
+      if (a.dstream) load_row<E, T, VEC>((const S *)a.dstream + row * a.ldds, t, j, a.cols, o);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) put(j, j, mean);
-    } else {
-      for (int j = 0; j < n; ++j) {
-        take(j, 0);
-        if (ds) load_row<E, T, VEC>(ds, t, j, a.cols, o[0]);
-        join(0, false);
-        put(j, 0, mean);
+      for (int i = 0; i < 8; ++i) {
+        g[i] = (g[i] * w[i] - xh[i] * mean) * rstd;
+        if (a.dstream) g[i] += o[i];
       }
+      store_row<E, T, VEC>((S *)a.dx + row * a.lddx, t, j, a.cols, g);
     }
-  }
-  if (NV) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) store_row<F32, T, VEC>(partial, t, j, a.cols, dw[j]);
   }
 }
 
-// out[c] = sum over g of partial[g][c], always in the same order: 32 columns
-// a workgroup, 8 threads a column.
-__global__ __launch_bounds__(256) void fold_kernel(const float *partial, int groups, int64_t cols, float *out) {
-  __shared__ float part[8][32];
-  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
-  const int lane = threadIdx.x / 32;
+// out[c] = sum over g of partial[g][c], always in the same order: 16 columns
+// (64 bytes of a row) a workgroup, 64 threads a column, so that a few thousand
+// columns already fill the chip.
+__global__ __launch_bounds__(1024) void fold_kernel(const float *partial, int groups, int64_t cols, float *out) {
+  __shared__ float part[64][17];
+  const int64_t c = (int64_t)blockIdx.x * 16 + threadIdx.x % 16;
+  const int lane = threadIdx.x / 16;
   float s = 0.f;
-  if (c < cols)
-    for (int g = lane; g < groups; g += 8) s += partial[(int64_t)g * cols + c];
-  part[lane][threadIdx.x % 32] = s;
-  __syncthreads();
-  if (lane == 0 && c < cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
-    out[c] = s;
+  if (c < cols) {
+#pragma unroll 8
+    for (int g = lane; g < groups; g += 64) s += partial[(int64_t)g * cols + c];
   }
+  part[lane][threadIdx.x % 16] = s;
+#pragma unroll
+  for (int half = 32; half; half /= 2) {
+    __syncthreads();
+    if (lane < half) part[lane][threadIdx.x % 16] += part[lane + half][threadIdx.x % 16];
+  }
+  if (lane == 0 && c < cols) out[c] = part[0][threadIdx.x];
 }
 
 // Dropout.  Element i of the row-major array takes 16 bits of the generator's
@@ -609,12 +667,11 @@ void norm_grad_go(const NormGradArgs &a, hipStream_t s) {
 template <class E>
 void norm_grad_by_length(const NormGradArgs &a, hipStream_t s) {
   if (a.cols <= 512) norm_grad_go<E, 64, 1>(a, s);
-  else if (a.cols <= 1024) norm_grad_go<E, 64, 2>(a, s);
   else if (a.cols <= 2048) norm_grad_go<E, 256, 1>(a, s);
   else if (a.cols <= 4096) norm_grad_go<E, 256, 2>(a, s);
   else if (a.cols <= 8192) norm_grad_go<E, 1024, 1>(a, s);
-  else if (a.cols <= 16384) norm_grad_go<E, 1024, 2>(a, s);
-  else norm_grad_go<E, 1024, 0>(a, s);
+  else if (a.vec) norm_grad_long_kernel<E, true><<<(unsigned)a.groups, 1024, 0, s>>>(a);
+  else norm_grad_long_kernel<E, false><<<(unsigned)a.groups, 1024, 0, s>>>(a);
 }
 
 template <class E>
@@ -649,7 +706,7 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
 int norm_grad_groups(int64_t rows, int64_t cols) {
   // enough workgroups for the memory to be kept busy (4 of 256 threads a
   // compute unit, 2 of 1024), and no more partial rows than that
-  const int64_t most = cols <= 1024 ? 4096 : cols <= 4096 ? 1024 : 512;
+  const int64_t most = cols <= 512 ? 4096 : cols <= 4096 ? 1024 : 512;
   return (int)(rows < 1 ? 1 : rows < most ? rows : most);
 }
 
@@ -662,7 +719,7 @@ hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_column_fold(const float *partial, int groups, int64_t cols, float *out, hipStream_t s) {
-  fold_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(partial, groups, cols, out);
+  fold_kernel<<<(unsigned)((cols + 15) / 16), 1024, 0, s>>>(partial, groups, cols, out);
   return hipGetLastError();
 }
 
