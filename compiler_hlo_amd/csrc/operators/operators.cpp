@@ -2,6 +2,7 @@
 // and its split, the workspace's layout, and the launches.
 #include "operators.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <memory>
@@ -47,6 +48,7 @@ struct Product {
   bool a_by_col = false, b_by_col = false, gated = false;
   int64_t m = 0, n = 0, k = 0;
   int tile = 0, splits = 1, per_split = 1, waves = 8;
+  int64_t tiles_full = 0, part_rows = 0, part_cols = 0;
   int64_t partial_at = 0, ldp = 0;
 };
 
@@ -139,6 +141,41 @@ Operand operand(hf_operator &op, int64_t rows, int64_t cols, int64_t ld, int64_t
   return o;
 }
 
+int64_t tiles_of(const Product &p, int64_t tile) { return cdiv(p.m, tile) * cdiv(p.n, p.gated ? tile / 2 : tile); }
+
+// The tile, and how the last tiles are shared: the shortest time by a simple
+// account, in microseconds.  A round of tiles (256 of the larger, 512 of the
+// smaller, two a compute unit) takes its stages and an end (sums out, the next
+// tile's first loads in); sharing costs a launch and the partial sums' way to
+// memory and back.  The constants are fits to bf16 and e4m3 products of
+// 128 .. 4099 rows with 4096 columns over 4096 .. 16384, all within 10%: a
+// stage takes 1.1 (1.35 with the chip full) in the larger tile, 0.6 (0.95 with
+// two a compute unit) in the smaller.  What it decides there: 4099 x 4096 x
+// 16384 e4m3, 272 large tiles, the last 16 shared by 8 workgroups each, 218
+// (303 unshared); 1024 x 4096 x 4096 small tiles, 41 (large 73); 256 x 4096 x
+// 4096 small tiles shared by 4, 22 (unshared 37).
+void choose_tiles(Product &p, int64_t steps, bool wide) {
+  double best = 1e300;
+  for (int tile = wide ? 1 : 0; tile < 2; ++tile) {
+    const int64_t t = tile == 0 ? 256 : 128, slots = tile == 0 ? 256 : 512, all = tiles_of(p, t);
+    const double full_stage = tile == 0 ? 1.35 : 0.95, end = tile == 0 ? 6.0 : 3.0;
+    const auto stage = [&](int64_t groups) { return groups <= slots / 2 ? (tile == 0 ? 1.1 : 0.6) : full_stage; };
+    const int64_t full = all / slots * slots, rest = all - full;
+    for (int64_t s = 1; s <= 16 && (s == 1 || (rest > 0 && rest * s <= slots && steps >= 2 * s)); ++s) {
+      double us = (double)(full / slots) * ((double)steps * full_stage + end);
+      if (rest > 0) us += (double)cdiv(steps, s) * stage(rest * s) + end;
+      if (s > 1) us += 3.0 + 2.0 * 4.0 * (double)(s * rest * std::min(t, p.m) * t) / 6e6;
+      if (us >= best) continue;
+      best = us;
+      p.tile = tile;
+      p.tiles_full = s > 1 ? full : all;
+      p.per_split = (int)std::max<int64_t>(1, cdiv(steps, s));
+      p.splits = s > 1 ? (int)cdiv(steps, p.per_split) : 1;
+      if (p.splits == 1) p.tiles_full = all;
+    }
+  }
+}
+
 // Which kernel, which tile and how many parts the contraction is split into.
 // m x n are the sums (gated: n gate and n up columns).
 void choose(hf_operator &op, Product &p, int64_t elem) {
@@ -170,14 +207,14 @@ void choose(hf_operator &op, Product &p, int64_t elem) {
     p.per_split = (int)cdiv(steps > 0 ? steps : 1, s);
     p.splits = steps > 0 ? (int)cdiv(steps, p.per_split) : 1;
   } else {
-    const int64_t steps = cdiv(p.k, 128 / elem);
-    auto tiles = [&](int64_t t) { return cdiv(p.m, t) * cdiv(p.n, p.gated ? t / 2 : t); };
-    p.tile = tiles(256) >= 192 && !wide ? 0 : 1;
-    int64_t s = 1;
-    if (p.tile == 1)
-      while (tiles(128) * s < 256 && steps >= 8 * s) s *= 2;
-    p.per_split = (int)cdiv(steps > 0 ? steps : 1, s);
-    p.splits = steps > 0 ? (int)cdiv(steps, p.per_split) : 1;
+    choose_tiles(p, cdiv(p.k, 128 / elem), wide);
+    if (p.splits > 1) {
+      const int64_t t = p.tile == 0 ? 256 : 128;
+      p.part_rows = p.m < t ? p.m : t;
+      p.part_cols = p.gated ? 2 * std::min(t / 2, up(p.n, 8)) : std::min(t, up(p.n, 8));
+      p.partial_at = take(op, (tiles_of(p, t) - p.tiles_full) * p.splits * p.part_rows * p.part_cols * 4);
+    }
+    return;
   }
   if (p.splits > 1) p.partial_at = take(op, (int64_t)p.splits * p.m * p.ldp * 4);
 }
@@ -443,6 +480,9 @@ hipError_t run_product(const Call &c, const Product &p, const void *a, const voi
   g.a_by_col = p.a_by_col;
   g.b_by_col = p.b_by_col;
   g.tile = p.tile;
+  g.tiles_full = (int)p.tiles_full;
+  g.part_rows = (int)p.part_rows;
+  g.part_cols = (int)p.part_cols;
   g.splits = p.splits;
   g.k_tiles_per_split = p.per_split;
   g.partial = p.splits > 1 ? (float *)(c.ws + p.partial_at) : nullptr;
@@ -450,8 +490,7 @@ hipError_t run_product(const Call &c, const Product &p, const void *a, const voi
   g.e = e;
   s.waves = p.waves;
   s.blocks_per_split = p.per_split;
-  HF_TRY(p.skinny ? launch_skinny(s, c.stream) : launch_product(g, c.stream));
-  return p.splits > 1 ? launch_product_fold(g.partial, p.splits, p.ldp, e, c.stream) : hipSuccess;
+  return p.skinny ? launch_skinny(s, c.stream) : launch_product(g, c.stream);
 }
 
 hipError_t run_norm(const Call &c) {

@@ -96,8 +96,12 @@ struct ProductArgs {
   int32_t dtype;
   bool a_by_col, b_by_col;   // the contraction runs over the operand's rows
   int32_t tile;              // 0: 256 x 256, 1: 128 x 128 (columns of the product), 2: strips, m <= 64 by row
+  int32_t tiles_full;        // tiles 0 and 1: so many are one workgroup's, the others `splits` workgroups'
   int32_t splits, k_tiles_per_split;
-  float *partial;            // [splits][m][ldp] when splits > 1
+  // splits > 1: [splits][shared tiles][part_rows][part_cols], the up half's
+  // columns after the gate's, or (strips, skinny) [splits][m][ldp]
+  float *partial;
+  int32_t part_rows, part_cols;
   int64_t ldp;
   Epilogue e;
 };
@@ -110,9 +114,10 @@ struct SkinnyArgs {
   int32_t waves;             // of a workgroup: 4, 8 or 16
   int32_t blocks_per_split;  // blocks of 512 contraction bytes
 };
+
 hipError_t launch_skinny(const SkinnyArgs &a, hipStream_t s);
 
-// Sum the splits' partials and run the epilogue.
+// Sum the partials of strips or of skinny products and run the epilogue.
 hipError_t launch_product_fold(const float *partial, int splits, int64_t ldp, const Epilogue &e, hipStream_t s);
 
 }  // namespace hf

@@ -144,6 +144,14 @@ struct Half {
   }
 };
 
+// Tile number `id`: columns of 4 tile rows.
+__device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &tm, int &tn) {
+  constexpr int G = 4;
+  const int group = id / (G * tiles_n), first = group * G, size = tiles_m - first < G ? tiles_m - first : G;
+  tm = first + (id - group * G * tiles_n) % size;
+  tn = (id - group * G * tiles_n) / size;
+}
+
 // A workgroup computes 2 HM x 2 HN sums, 128 contraction bytes a stage, two
 // stages in LDS: 256 x 256 with 8 waves, one workgroup a compute unit, or
 // 128 x 128 with 4 waves, two of them.  A wave has HM/2 x 32 sums in each
@@ -165,25 +173,30 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void product_kernel(Produ
   const bool gated = a.e.gated;
   const int tile_n = gated ? HN : 2 * HN;
   const int tiles_m = (a.m + 2 * HM - 1) / (2 * HM), tiles_n = (a.n + tile_n - 1) / tile_n;
+  // The first tiles_full tiles are a workgroup's each; the rest, which would
+  // leave most of the chip idle for a whole tile's time, are shared by
+  // `splits` workgroups each, one part of the contraction a workgroup.
+  const int tiles = tiles_m * tiles_n, rest = tiles - a.tiles_full;
+  const bool part = (int)blockIdx.x >= a.tiles_full;
   // Consecutive workgroups go to different XCDs; each XCD takes a contiguous
   // run of tiles, in columns of 4 tile rows, so that the tiles it works on at
   // a time share rows and columns in its L2.
-  const int tiles = tiles_m * tiles_n;
-  int id = blockIdx.x;
+  int id = part ? blockIdx.x - a.tiles_full : blockIdx.x;
   {
-    const int xcd = id % 8, q = tiles / 8, r = tiles % 8;
+    const int count = part ? rest * a.splits : a.tiles_full;
+    const int xcd = id % 8, q = count / 8, r = count % 8;
     id = xcd * q + (xcd < r ? xcd : r) + id / 8;
   }
-  constexpr int G = 4;
-  const int group = id / (G * tiles_n), first = group * G, size = tiles_m - first < G ? tiles_m - first : G;
-  const int tm = first + (id - group * G * tiles_n) % size, tn = (id - group * G * tiles_n) / size;
+  const int piece = part ? id / rest : 0, local = part ? id % rest : 0;
+  int tm, tn;
+  tile_at(part ? a.tiles_full + local : id, tiles_m, tiles_n, tm, tn);
   const int m0 = tm * 2 * HM, n0 = tn * tile_n;
 
   const int w = threadIdx.x / 64, wm = w / WN, wn = w % WN;
-  const int k0 = blockIdx.y * a.k_tiles_per_split;
   constexpr int kStep = 128 / Step::kBytes;  // elements of the contraction a stage
   const int all = (a.k + kStep - 1) / kStep;
-  const int kn = all - k0 < a.k_tiles_per_split ? all - k0 : a.k_tiles_per_split;
+  const int k0 = piece * a.k_tiles_per_split;
+  const int kn = !part || all - k0 < a.k_tiles_per_split ? all - k0 : a.k_tiles_per_split;
 
   // the operands' first bytes for this tile and what is left of them
   const int64_t a0 = ACOL ? (int64_t)m0 * Step::kBytes + (int64_t)k0 * kStep * a.lda
@@ -343,12 +356,11 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void product_kernel(Produ
       float v[8], u[8];
       load8<F32>(out + r * kPitch + c, v);
       if (gated) load8<F32>(out + r * kPitch + HN + c, u);
-      if (a.splits > 1) {
-        // partial sums: rows of ldp floats, the up half in their second half
-        if (m < a.m && n < a.n) {
-          float *p = a.partial + ((int64_t)blockIdx.y * a.m + m) * a.ldp + n;
+      if (part && a.splits > 1) {
+        if (i * HM + r < a.part_rows && c < (gated ? a.part_cols / 2 : a.part_cols)) {
+          float *p = a.partial + (((int64_t)piece * rest + local) * a.part_rows + i * HM + r) * a.part_cols + c;
           store8<F32>(p, v);
-          if (gated) store8<F32>(p + a.ldp / 2, u);
+          if (gated) store8<F32>(p + a.part_cols / 2, u);
         }
       } else {
         finish<8>(a.e, m, n, v, u);
@@ -495,16 +507,49 @@ __global__ __launch_bounds__(256) void product_fold_kernel(const float *partial,
   }
 }
 
+// The same for the shared tiles of product_kernel: 1/8 of a tile's rows a
+// workgroup.
+__global__ __launch_bounds__(256) void product_tile_fold_kernel(ProductArgs a, int size) {
+  const bool gated = a.e.gated;
+  const int tile_n = gated ? size / 2 : size, per = tile_n / 8;
+  const int tiles_m = (a.m + size - 1) / size, tiles_n = (a.n + tile_n - 1) / tile_n;
+  const int rest = tiles_m * tiles_n - a.tiles_full;
+  int tm, tn;
+  tile_at(a.tiles_full + blockIdx.x, tiles_m, tiles_n, tm, tn);
+  for (int at = threadIdx.x; at < size / 8 * per; at += 256) {
+    const int r = blockIdx.y * (size / 8) + at / per, c = at % per * 8, m = tm * size + r, n = tn * tile_n + c;
+    if (m >= a.m || n >= a.n) continue;
+    float v[8], u[8], x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+      const float *p = a.partial + (((int64_t)s * rest + blockIdx.x) * a.part_rows + r) * a.part_cols + c;
+      load8<F32>(p, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += x[i];
+      if (gated) {
+        load8<F32>(p + a.part_cols / 2, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] += x[i];
+      }
+    }
+    finish<8>(a.e, m, n, v, u);
+  }
+}
+
 template <class Step, bool ACOL, bool BCOL>
 hipError_t go(const ProductArgs &a, hipStream_t s) {
   const int64_t tile = a.tile == 0 ? 256 : 128, tile_n = a.e.gated ? tile / 2 : tile;
-  const dim3 grid((unsigned)(((a.m + tile - 1) / tile) * ((a.n + tile_n - 1) / tile_n)), (unsigned)a.splits);
+  const int64_t rest = ((a.m + tile - 1) / tile) * ((a.n + tile_n - 1) / tile_n) - a.tiles_full;
+  const unsigned grid = (unsigned)(a.tiles_full + rest * a.splits);
   if (a.tile == 0) {
     if constexpr (Step::kWide) return hipErrorInvalidValue;  // never planned
     else product_kernel<Step, ACOL, BCOL, 128, 128><<<grid, 512, 0, s>>>(a);
   } else {
     product_kernel<Step, ACOL, BCOL, 64, 64><<<grid, 256, 0, s>>>(a);
   }
+  if (rest > 0 && a.splits > 1)
+    product_tile_fold_kernel<<<dim3((unsigned)rest, 8), 256, 0, s>>>(a, (int)tile);
   return hipGetLastError();
 }
 
@@ -512,7 +557,8 @@ template <class Step>
 hipError_t go_strip(const ProductArgs &a, hipStream_t s) {
   const int width = a.e.gated ? 128 : 256;
   strip_kernel<Step><<<dim3((unsigned)((a.n + width - 1) / width), (unsigned)a.splits), 512, 0, s>>>(a);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || a.splits == 1 ? e : launch_product_fold(a.partial, a.splits, a.ldp, a.e, s);
 }
 
 template <class Step>

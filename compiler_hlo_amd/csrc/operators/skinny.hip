@@ -147,7 +147,8 @@ hipError_t go(const SkinnyArgs &a, hipStream_t s) {
   if (a.waves == 16) skinny_kernel<Step, GATED, 16><<<grid, 1024, 0, s>>>(a);
   else if (a.waves == 8) skinny_kernel<Step, GATED, 8><<<grid, 512, 0, s>>>(a);
   else skinny_kernel<Step, GATED, 4><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || a.p.splits == 1 ? e : launch_product_fold(a.p.partial, a.p.splits, a.p.ldp, a.p.e, s);
 }
 
 template <class Step>
