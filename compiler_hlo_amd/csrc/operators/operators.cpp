@@ -200,12 +200,22 @@ void choose(hf_operator &op, Product &p, int64_t elem) {
     p.splits = blocks > 0 ? (int)cdiv(blocks, p.per_split) : 1;
   } else if (!p.a_by_col && !p.b_by_col && p.m <= 64) {
     p.tile = 2;
+    // Shares of the contraction: the shortest time by an account like that of
+    // the tiles.  A stage takes its share of the memory's rate, or the latency
+    // that two stages in flight leave where there are few workgroups (fits to
+    // 16 .. 64 rows; 24 x 22528 x 4096 by 2: 41 us, unshared 52; 64 x 4096 x
+    // 4096 by 8: 16 us, unshared 42, by 16 21).
     const int64_t strips = cdiv(p.n, p.gated ? 128 : 256), steps = cdiv(p.k, 128 / elem);
-    // one workgroup a compute unit, with at least 4 stages of the contraction
-    int64_t s = strips < 256 ? 256 / strips : 1;
-    if (s > steps / 4) s = steps / 4 > 0 ? steps / 4 : 1;
-    p.per_split = (int)cdiv(steps > 0 ? steps : 1, s);
-    p.splits = steps > 0 ? (int)cdiv(steps, p.per_split) : 1;
+    double best = 1e300;
+    for (int64_t s = 1; s <= 32 && (s == 1 || (strips * s <= 256 && steps >= 2 * s)); ++s) {
+      const double stage = std::max(0.6 + 0.0035 * (double)p.m, 0.0065 * (double)std::min<int64_t>(strips * s, 256));
+      double us = (double)cdiv(strips * s, 256) * ((double)cdiv(steps, s) * stage + 3.0);
+      if (s > 1) us += 3.5 + 8.0 * (double)(s * p.m * p.ldp) / 5e6;
+      if (us >= best) continue;
+      best = us;
+      p.per_split = (int)std::max<int64_t>(1, cdiv(steps, s));
+      p.splits = steps > 0 ? (int)cdiv(steps, p.per_split) : 1;
+    }
   } else {
     choose_tiles(p, cdiv(p.k, 128 / elem), wide);
     if (p.splits > 1) {
