@@ -154,7 +154,7 @@ int64_t tiles_of(const Product &p, int64_t tile) { return cdiv(p.m, tile) * cdiv
 // 16384 e4m3, 272 large tiles, the last 16 shared by 8 workgroups each, 218
 // (303 unshared); 1024 x 4096 x 4096 small tiles, 41 (large 73); 256 x 4096 x
 // 4096 small tiles shared by 4, 22 (unshared 37).
-void choose_tiles(Product &p, int64_t steps, bool wide) {
+double choose_tiles(Product &p, int64_t steps, bool wide) {
   double best = 1e300;
   for (int tile = wide ? 1 : 0; tile < 2; ++tile) {
     const int64_t t = tile == 0 ? 256 : 128, slots = tile == 0 ? 256 : 512, all = tiles_of(p, t);
@@ -174,19 +174,23 @@ void choose_tiles(Product &p, int64_t steps, bool wide) {
       if (p.splits == 1) p.tiles_full = all;
     }
   }
+  return best;
 }
 
 // Which kernel, which tile and how many parts the contraction is split into.
-// m x n are the sums (gated: n gate and n up columns).
-void choose(hf_operator &op, Product &p, int64_t elem) {
+// m x n are the sums (gated: n gate and n up columns).  Returns the time that
+// it accounts for, in microseconds.
+double choose(const hf_operator_desc &d, Product &p, int64_t elem) {
   p.on = p.m > 0 && p.n > 0;
-  if (!p.on) return;
+  if (!p.on) return 0.0;
+  double best = 1e300;
   const int64_t kbytes = p.k * elem;
   p.ldp = p.gated ? 2 * up(p.n, 8) : up(p.n, 8);
+  p.skinny = false;
   p.splits = 1;
   // e4m3 widened to 16 bits has no registers to spare for the larger tile or
   // for 16 waves a workgroup
-  const bool wide = op.d.dtype == HF_F8E4M3 && f8_wide(op.d.out_dtype, p.k);
+  const bool wide = d.dtype == HF_F8E4M3 && f8_wide(d.out_dtype, p.k);
   if (!p.a_by_col && !p.b_by_col && p.m <= 8) {
     p.skinny = true;
     const int64_t columns = cdiv(p.n, 16), blocks = cdiv(kbytes, 512);
@@ -198,6 +202,7 @@ void choose(hf_operator &op, Product &p, int64_t elem) {
     while (columns * s < 256 && blocks >= 2 * s * p.waves) s *= 2;
     p.per_split = (int)cdiv(blocks > 0 ? blocks : 1, s);
     p.splits = blocks > 0 ? (int)cdiv(blocks, p.per_split) : 1;
+    best = 4.0 + (double)((p.gated ? 2 : 1) * p.n * kbytes) / 5e6;
   } else if (!p.a_by_col && !p.b_by_col && p.m <= 64) {
     p.tile = 2;
     // Shares of the contraction: the shortest time by an account like that of
@@ -206,7 +211,6 @@ void choose(hf_operator &op, Product &p, int64_t elem) {
     // 16 .. 64 rows; 24 x 22528 x 4096 by 2: 41 us, unshared 52; 64 x 4096 x
     // 4096 by 8: 16 us, unshared 42, by 16 21).
     const int64_t strips = cdiv(p.n, p.gated ? 128 : 256), steps = cdiv(p.k, 128 / elem);
-    double best = 1e300;
     for (int64_t s = 1; s <= 32 && (s == 1 || (strips * s <= 256 && steps >= 2 * s)); ++s) {
       const double stage = std::max(0.6 + 0.0035 * (double)p.m, 0.0065 * (double)std::min<int64_t>(strips * s, 256));
       double us = (double)cdiv(strips * s, 256) * ((double)cdiv(steps, s) * stage + 3.0);
@@ -217,16 +221,21 @@ void choose(hf_operator &op, Product &p, int64_t elem) {
       p.splits = steps > 0 ? (int)cdiv(steps, p.per_split) : 1;
     }
   } else {
-    choose_tiles(p, cdiv(p.k, 128 / elem), wide);
-    if (p.splits > 1) {
-      const int64_t t = p.tile == 0 ? 256 : 128;
-      p.part_rows = p.m < t ? p.m : t;
-      p.part_cols = p.gated ? 2 * std::min(t / 2, up(p.n, 8)) : std::min(t, up(p.n, 8));
-      p.partial_at = take(op, (tiles_of(p, t) - p.tiles_full) * p.splits * p.part_rows * p.part_cols * 4);
-    }
-    return;
+    best = choose_tiles(p, cdiv(p.k, 128 / elem), wide);
+    const int64_t t = p.tile == 0 ? 256 : 128;
+    p.part_rows = p.m < t ? p.m : t;
+    p.part_cols = p.gated ? 2 * std::min(t / 2, up(p.n, 8)) : std::min(t, up(p.n, 8));
   }
-  if (p.splits > 1) p.partial_at = take(op, (int64_t)p.splits * p.m * p.ldp * 4);
+  return best;
+}
+
+// The partial sums' place, for what choose() chose.
+void place_partials(hf_operator &op, Product &p) {
+  if (!p.on || p.splits == 1) return;
+  const bool tiles = !p.skinny && p.tile < 2;
+  const int64_t sums = tiles ? (tiles_of(p, p.tile == 0 ? 256 : 128) - p.tiles_full) * p.part_rows * p.part_cols
+                             : p.m * p.ldp;
+  p.partial_at = take(op, p.splits * sums * 4);
 }
 
 void plan_norm(hf_operator &op) {
@@ -312,7 +321,23 @@ void plan_product(hf_operator &op) {
     p.b = operand(op, wide, d.k, op.buf[1].ld, elem, "b");
     p.k = p.a.pack_at >= 0 || p.b.pack_at >= 0 ? up(d.k, 16 / elem) : d.k;
   }
-  choose(op, p, elem);
+  const double whole = choose(d, p, elem);
+  // A few rows past a multiple of 256 cost a row of tiles; where a strip (or a
+  // skinny product) for them is shorter, they get one (4099 x 4096 x 16384
+  // e4m3: 222 us with them in tiles, 207 us so).
+  const int64_t tail = d.m % 256;
+  if (d.m > 256 && tail > 0 && tail <= 64 && p.n > 0) {
+    Product body = p, rest = p;
+    body.m = d.m - tail;
+    body.a.rows = body.m;
+    rest.m = rest.a.rows = tail;
+    if (choose(d, body, elem) + choose(d, rest, elem) < whole) {
+      op.p1 = body;
+      op.p2 = rest;
+    }
+  }
+  place_partials(op, op.p1);
+  place_partials(op, op.p2);
 }
 
 void plan_product_grad(hf_operator &op) {
@@ -358,7 +383,8 @@ void plan_product_grad(hf_operator &op) {
   p.b_by_col = true;
   if (op.dz_at >= 0) p.k = op.lddz;  // whole 16-byte chunks; past `wide`, zeros on both sides
   p.a.cols = p.k;
-  choose(op, p, elem);
+  choose(d, p, elem);
+  place_partials(op, p);
   // db [wide, k] = dz^T [wide, m] a [m, k]
   Product &q = op.p2;
   q.m = wide;
@@ -369,7 +395,8 @@ void plan_product_grad(hf_operator &op) {
   q.a.cols = up(wide, 8);
   q.b = a;
   q.a_by_col = q.b_by_col = true;
-  choose(op, q, elem);
+  choose(d, q, elem);
+  place_partials(op, q);
 }
 
 void make_plan(hf_operator &op) {
@@ -588,9 +615,22 @@ hipError_t run_product_forward(const Call &c) {
   e.gated = op.p1.gated;
   e.vec = op.vec;
   const void *a, *b;
-  HF_TRY(place(c, op.p1.a, c.in(0), elem, &a));
+  Operand all = op.p1.a;
+  all.rows = op.d.m;
+  HF_TRY(place(c, all, c.in(0), elem, &a));
   HF_TRY(place(c, op.p1.b, c.in(1), elem, &b));
-  return run_product(c, op.p1, a, b, elem, e);
+  e.m = (int)op.p1.m;
+  HF_TRY(run_product(c, op.p1, a, b, elem, e));
+  if (!op.p2.on) return hipSuccess;
+  // the last rows: the same product from their first on
+  const int64_t from = op.p1.m, out = op.buf[d].elem();
+  a = (const char *)a + from * op.p1.a.ld * elem;
+  e.m = (int)op.p2.m;
+  e.d = (char *)e.d + from * e.ldd * out;
+  if (e.z) e.z = (char *)e.z + from * e.ldz * out;
+  if (e.residual) e.residual = (const char *)e.residual + from * e.ldr * out;
+  if (e.a_scale) e.a_scale += from;
+  return run_product(c, op.p2, a, b, elem, e);
 }
 
 hipError_t run_product_grad(const Call &c) {

@@ -87,15 +87,33 @@ __device__ __forceinline__ void load_weight(const void *w, bool wide, int t, int
     load_row<E, T, VEC>((const typename E::Store *)w, t, j, cols, v);
 }
 
+// One step of a wave's reduction: the value of the lane that CTRL (a data
+// parallel primitive's control) names, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, true);
+}
+
+// Over a wave: within rows of 16 lanes by shifts of 1, 2, 4 and 8, then row 0
+// into 1 and 2 into 3, then the first half into the second; lane 63 has it
+// all.  0 is neutral to both operations.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+  v += __uint_as_float(moved<0x111, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x112, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x114, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x118, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x142, 0xa>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x143, 0xc>(__float_as_uint(v)));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
-  return v;
+  v = max(v, moved<0x111, 0xf>(v));
+  v = max(v, moved<0x112, 0xf>(v));
+  v = max(v, moved<0x114, 0xf>(v));
+  v = max(v, moved<0x118, 0xf>(v));
+  v = max(v, moved<0x142, 0xa>(v));
+  v = max(v, moved<0x143, 0xc>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // Over the T threads of a row.  `slots`: T/64 floats of this call's own (no
@@ -179,7 +197,7 @@ __device__ __forceinline__ void store_row8(uint8_t *row, int t, int j, int cols,
   const u32x2 p = pack8<OUT>(v);
   if (VEC) {
     const int c = column<T, VEC>(t, j, 0);
-    if (c < cols) *(u32x2 *)(row + c) = p;
+    if (c < cols) __builtin_nontemporal_store(p, (u32x2 *)(row + c));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -223,16 +241,26 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a) {
     }
   };
   auto take = [&](int j, float (&h)[8]) {
-    input(j, h);
     if (stream) store_row<E, T, VEC>(stream, t, j, a.cols, h);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[i], h[i], sum);
   };
+  // The weight is asked for together with the row, not after its sum: with a
+  // single row the two latencies would add up.
+  const bool wide = a.weight_dtype == HF_F32;
+  float w[NV ? NV : 1][8];
   if (NV) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) input(j, keep[j]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w[j]);
 #pragma unroll
     for (int j = 0; j < NV; ++j) take(j, keep[j]);
   } else {
-    for (int j = 0; j < n; ++j) take(j, keep[0]);
+    for (int j = 0; j < n; ++j) {
+      input(j, keep[0]);
+      take(j, keep[0]);
+    }
   }
   sum = row_sum<T>(sum, slots);
   const float m = sum / (float)a.cols + a.eps;
@@ -286,12 +314,10 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a) {
     rstd = far ? ldexpf(1.0f / sqrtf(again / (float)a.cols + root * root), 1 - power) : 1.0f / sqrtf(m);
   }
   if (a.rstd && t == 0) a.rstd[row] = rstd;
-  const bool wide = a.weight_dtype == HF_F32;
   auto scaled = [&](int j, float (&h)[8]) {
-    float w[8];
-    load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w);
+    if (!NV) load_weight<E, T, VEC>(a.weight, wide, t, j, a.cols, w[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = h[i] * rstd * w[i];
+    for (int i = 0; i < 8; ++i) h[i] = h[i] * rstd * w[NV ? j : 0][i];
   };
   if (OUT < 0) {
     S *y = (S *)a.y + row * a.ldy;
@@ -660,7 +686,7 @@ void norm_grad_go(const NormGradArgs &a, hipStream_t s) {
   const unsigned block = T == 64 ? 256 : T;
   if (a.vec)
     norm_grad_kernel<E, T, NV, true><<<grid, block, 0, s>>>(a);
-  else
+  else if constexpr (NV < 4)
     norm_grad_kernel<E, T, NV, false><<<grid, block, 0, s>>>(a);
 }
 
@@ -670,6 +696,7 @@ void norm_grad_by_length(const NormGradArgs &a, hipStream_t s) {
   else if (a.cols <= 2048) norm_grad_go<E, 256, 1>(a, s);
   else if (a.cols <= 4096) norm_grad_go<E, 256, 2>(a, s);
   else if (a.cols <= 8192) norm_grad_go<E, 1024, 1>(a, s);
+  else if (a.cols <= 16384 && a.vec && E::kBytes == 2) norm_grad_go<E, E::kBytes == 2 ? 512 : 1024, E::kBytes == 2 ? 4 : 1>(a, s);
   else if (a.vec) norm_grad_long_kernel<E, true><<<(unsigned)a.groups, 1024, 0, s>>>(a);
   else norm_grad_long_kernel<E, false><<<(unsigned)a.groups, 1024, 0, s>>>(a);
 }
@@ -705,8 +732,8 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
 
 int norm_grad_groups(int64_t rows, int64_t cols) {
   // enough workgroups for the memory to be kept busy (4 of 256 threads a
-  // compute unit, 2 of 1024), and no more partial rows than that
-  const int64_t most = cols <= 512 ? 4096 : cols <= 4096 ? 1024 : 512;
+  // compute unit, 2 of 1024, 1 of 512), and no more partial rows than that
+  const int64_t most = cols <= 512 ? 4096 : cols <= 4096 ? 1024 : cols <= 8192 ? 512 : 256;
   return (int)(rows < 1 ? 1 : rows < most ? rows : most);
 }
 

@@ -708,7 +708,9 @@ def test_launch_refusals():
     refused([A, B + 16], [B], "overlaps b")
     # an extent that runs past its allocation
     whole = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
-    end = whole.data_ptr() + whole.numel()
+    # (torch may have cut the tensor from a larger one: its allocation's end)
+    end = [g["address"] + g["total_size"] for g in torch.cuda.memory_snapshot()
+           if g["address"] <= whole.data_ptr() < g["address"] + g["total_size"]][0]
     refused([end - 16, B], [D], "past the end")
     split = H.Matmul(100, 256, 4096, "bf16")
     assert split.workspace_bytes > 0
@@ -744,3 +746,29 @@ def test_column_windows_of_one_array():
     assert torch.equal(base[:, :128], x)
     with pytest.raises(H.FusionError):
         op(base[:, :128], w, out=[base[:, 64:192], rstd])
+
+
+@pytest.mark.parametrize("m, n, k", [(2050, 4096, 512), (4099, 2048, 640), (4160, 2080, 264)])
+def test_matmul_last_rows(m, n, k):
+    """A few rows past whole tiles, which may be a strip of their own: every
+    operand and result of theirs lies at an offset."""
+    for dtype, out, act in (("bf16", "bf16", "silu"), ("f8e4m3", "f16", None)):
+        say("matmul", dtype, m, n, k)
+        g = gen(m + k)
+        ops = operands(g, m, n, k, dtype)
+        extra = {"bias": normal(g, (n,), out), "residual": normal(g, (m, n), out, stride=n + 16)}
+        op = H.Matmul(m, n, k, dtype, out_dtype=out, bias=True, activation=act, residual=True, save=True,
+                      strides={"residual": n + 16, "z": n + 8})
+        check_matmul(ops, extra, op(*ops, *extra.values()), out, act, True)
+
+
+def test_gated_last_rows():
+    m, n, k = 2060, 2048, 320
+    g = gen(m)
+    ops = operands(g, m, 2 * n, k, "s8")
+    d, zs = H.GatedFeedForward(m, n, k, "s8", out_dtype="f16", activation="relu", save=True)(*ops)
+    z, mag = sums(ops)
+    err = R.sum_error(mag, k) + 4 * 2.0 ** -24 * mag
+    R.close(zs, z, err, torch.float16)
+    f, u = R.act("relu", z[:, :n])[0], z[:, n:]
+    R.close(d, f * u, err[:, :n] * (u.abs() + err[:, n:]) + f.abs() * err[:, n:] + (f * u).abs() * 2.0 ** -24, torch.float16)
