@@ -1,0 +1,65 @@
+"""examples/feed_forward.py: the layer's values and gradients against a plain
+64-bit form, its training under a graph, and its 8-bit serving."""
+import os
+import sys
+
+import pytest
+import torch
+
+import operators_reference as R
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+pytestmark = pytest.mark.gpu
+
+
+def relative(got, want):
+    return float((R.f64(got) - want).norm() / want.norm())
+
+
+def test_layer_against_autograd_in_64_bits():
+    """Without dropout.  Each tensor between the operators is rounded to bf16
+    (2^-9 of its norm, a random rounding's size); six of them lie on the
+    longest path."""
+    import feed_forward as F
+    rows, hidden, inner = 200, 256, 384
+    layer = F.TrainingStep(rows, hidden, inner, p=0.0)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    layer.x.copy_(torch.randn(layer.x.shape, generator=g, device="cuda"))
+    layer.target.copy_(torch.randn(layer.x.shape, generator=g, device="cuda"))
+    layer.forward(), layer.backward()
+    x, wn, wg, wd = (R.f64(t).requires_grad_() for t in (layer.x, *layer.weight.values()))
+    h = x * (x.square().mean(1, keepdim=True) + 1e-5).rsqrt() * wn
+    z = h @ wg.T
+    y = x + (torch.nn.functional.silu(z[:, :inner]) * z[:, inner:]) @ wd.T
+    (0.5 * (y - R.f64(layer.target)).square().sum() / rows).backward()
+    assert relative(layer.y, y.detach()) < 6 * 2.0 ** -9
+    for got, want in ((layer.dx, x), (layer.grad_norm, wn), (layer.grad_gate_up, wg), (layer.grad_down, wd)):
+        assert relative(got, want.grad) < 6 * 2.0 ** -9
+
+
+def test_training_lowers_the_loss_and_serving_agrees():
+    import feed_forward as F
+    layer = F.TrainingStep(300, 256, 512, p=0.1)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    layer.x.copy_(torch.randn(layer.x.shape, generator=g, device="cuda"))
+    layer.target.copy_(layer.x.roll(1, 1))
+    layer.step(0.05)
+    first = layer.loss()
+    for _ in range(40):
+        layer.step(0.05)
+    assert layer.loss() < 0.9 * first
+    for kind, step in (("f8e4m3", 2.0 ** -4), ("s8", 4.0 / 127)):
+        served = F.Served(layer.master, kind)
+        for rows in (1, 20, 300):
+            x = layer.x[:rows].contiguous()
+            y, stream = served(x, torch.zeros_like(x))
+            assert torch.equal(stream, x)
+            w = {k: R.f64(v) for k, v in layer.master.items()}
+            v = R.f64(x)
+            h = v * (v.square().mean(1, keepdim=True) + 1e-5).rsqrt() * w["norm"]
+            z = h @ w["gate_up"].T
+            want = (torch.nn.functional.silu(z[:, :512]) * z[:, 512:]) @ w["down"].T
+            # two operands quantised by at most half a step each, through a
+            # product of two such sums
+            assert relative(R.f64(y) - v, want) < 4 * step
