@@ -37,6 +37,17 @@ struct F32 {
   static __device__ __forceinline__ Store store(float f) { return f; }
 };
 
+// Launches a kernel and returns this launch's own error.
+template <class T>
+struct Same {
+  typedef T Type;
+};
+template <class... P>
+inline hipError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, hipStream_t s, typename Same<P>::Type... args) {
+  void *pointers[] = {&args...};
+  return hipLaunchKernel((const void *)kernel, grid, dim3(block), pointers, 0, s);
+}
+
 // Eight consecutive elements as 32-bit floats: one 16-byte access in the
 // 16-bit types, two in f32.  p is 16-byte aligned.
 template <class T>

@@ -410,6 +410,10 @@ void make_plan(hf_operator &op) {
     if (v < 0) invalid(who + ": a negative size");
   for (int64_t v : {d.m, d.n, d.k})
     if (v > most) unsupported(who + ": a size of 2^31 or more");
+  // columns and tiles are counted in 32 bits, with room for a tile's padding
+  const int64_t wide_most = int64_t(1) << 30;
+  if (d.kind != HF_OPERATOR_DROPOUT && d.n > wide_most) unsupported(who + ": more than 2^30 columns");
+  if (product && (d.m > wide_most || d.k > wide_most)) unsupported(who + ": a size of more than 2^30");
   if (!product && d.k != 0) invalid(who + ": k must be 0");
   static const uint32_t allowed[] = {HF_OPERATOR_RESIDUAL, HF_OPERATOR_RESIDUAL,
                                      HF_OPERATOR_RESIDUAL | HF_OPERATOR_BIAS | HF_OPERATOR_SAVE, HF_OPERATOR_BIAS,
@@ -424,8 +428,8 @@ void make_plan(hf_operator &op) {
     if (!ok) unsupported(who + ": operands of this element type");
     if (grad ? d.out_dtype != d.dtype : !is_half(d.out_dtype) && d.out_dtype != HF_F32)
       unsupported(who + ": results of this element type");
-    if ((d.kind == HF_OPERATOR_GATED || d.kind == HF_OPERATOR_GATED_GRAD) && 2 * d.n > most)
-      unsupported(who + ": 2n of 2^31 or more");
+    if ((d.kind == HF_OPERATOR_GATED || d.kind == HF_OPERATOR_GATED_GRAD) && 2 * d.n > wide_most)
+      unsupported(who + ": 2n of more than 2^30");
     if (d.dtype == HF_S8 && d.k >= (1 << 17)) unsupported(who + ": s8 sums over k >= 2^17 do not fit 32 bits");
   } else {
     if (!is_half(d.dtype) && d.dtype != HF_F32) unsupported(who + ": this element type");

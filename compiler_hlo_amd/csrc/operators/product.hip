@@ -542,22 +542,21 @@ hipError_t go(const ProductArgs &a, hipStream_t s) {
   const int64_t tile = a.tile == 0 ? 256 : 128, tile_n = a.e.gated ? tile / 2 : tile;
   const int64_t rest = ((a.m + tile - 1) / tile) * ((a.n + tile_n - 1) / tile_n) - a.tiles_full;
   const unsigned grid = (unsigned)(a.tiles_full + rest * a.splits);
-  if (a.tile == 0) {
-    if constexpr (Step::kWide) return hipErrorInvalidValue;  // never planned
-    else product_kernel<Step, ACOL, BCOL, 128, 128><<<grid, 512, 0, s>>>(a);
-  } else {
-    product_kernel<Step, ACOL, BCOL, 64, 64><<<grid, 256, 0, s>>>(a);
+  hipError_t e = hipErrorInvalidValue;
+  if (a.tile == 1) {
+    e = launch(product_kernel<Step, ACOL, BCOL, 64, 64>, grid, 256, s, a);
+  } else if constexpr (!Step::kWide) {  // never planned with kWide
+    e = launch(product_kernel<Step, ACOL, BCOL, 128, 128>, grid, 512, s, a);
   }
-  if (rest > 0 && a.splits > 1)
-    product_tile_fold_kernel<<<dim3((unsigned)rest, 8), 256, 0, s>>>(a, (int)tile);
-  return hipGetLastError();
+  if (e != hipSuccess || rest == 0 || a.splits == 1) return e;
+  return launch(product_tile_fold_kernel, dim3((unsigned)rest, 8), 256, s, a, (int)tile);
 }
 
 template <class Step>
 hipError_t go_strip(const ProductArgs &a, hipStream_t s) {
   const int width = a.e.gated ? 128 : 256;
-  strip_kernel<Step><<<dim3((unsigned)((a.n + width - 1) / width), (unsigned)a.splits), 512, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
+  const dim3 grid((unsigned)((a.n + width - 1) / width), (unsigned)a.splits);
+  const hipError_t e = launch(strip_kernel<Step>, grid, 512, s, a);
   return e != hipSuccess || a.splits == 1 ? e : launch_product_fold(a.partial, a.splits, a.ldp, a.e, s);
 }
 
@@ -584,8 +583,7 @@ hipError_t launch_product(const ProductArgs &a, hipStream_t s) {
 
 hipError_t launch_product_fold(const float *partial, int splits, int64_t ldp, const Epilogue &e, hipStream_t s) {
   const dim3 grid((unsigned)((e.n + 2047) / 2048), (unsigned)(e.m < 65535 ? e.m : 65535));
-  product_fold_kernel<<<grid, 256, 0, s>>>(partial, splits, ldp, e);
-  return hipGetLastError();
+  return launch(product_fold_kernel, grid, 256, s, partial, splits, ldp, e);
 }
 
 }  // namespace hf

@@ -650,84 +650,77 @@ __global__ __launch_bounds__(256) void pack_kernel(const S *src, int64_t ld_src,
 }
 
 template <class E, int OUT, int T, int NV>
-void norm_go(const NormArgs &a, hipStream_t s) {
+hipError_t norm_go(const NormArgs &a, hipStream_t s) {
   const int per = T == 64 ? 4 : 1;
-  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
-  const unsigned block = T == 64 ? 256 : T;
-  if (a.vec)
-    norm_kernel<E, OUT, T, NV, true><<<grid, block, 0, s>>>(a);
-  else
-    norm_kernel<E, OUT, T, NV, false><<<grid, block, 0, s>>>(a);
+  const dim3 grid((unsigned)((a.rows + per - 1) / per));
+  return launch(a.vec ? norm_kernel<E, OUT, T, NV, true> : norm_kernel<E, OUT, T, NV, false>, grid, T == 64 ? 256 : T,
+                s, a);
 }
 
 template <class E, int OUT>
-void norm_by_length(const NormArgs &a, hipStream_t s) {
-  if (a.cols <= 512) norm_go<E, OUT, 64, 1>(a, s);
-  else if (a.cols <= 1024) norm_go<E, OUT, 64, 2>(a, s);
-  else if (a.cols <= 2048) norm_go<E, OUT, 256, 1>(a, s);
-  else if (a.cols <= 4096) norm_go<E, OUT, 256, 2>(a, s);
-  else if (a.cols <= 8192) norm_go<E, OUT, 256, 4>(a, s);
-  else if (a.cols <= 16384) norm_go<E, OUT, 1024, 2>(a, s);
-  else if (a.cols <= 32768) norm_go<E, OUT, 1024, 4>(a, s);
-  else norm_go<E, OUT, 1024, 0>(a, s);
+hipError_t norm_by_length(const NormArgs &a, hipStream_t s) {
+  if (a.cols <= 512) return norm_go<E, OUT, 64, 1>(a, s);
+  if (a.cols <= 1024) return norm_go<E, OUT, 64, 2>(a, s);
+  if (a.cols <= 2048) return norm_go<E, OUT, 256, 1>(a, s);
+  if (a.cols <= 4096) return norm_go<E, OUT, 256, 2>(a, s);
+  if (a.cols <= 8192) return norm_go<E, OUT, 256, 4>(a, s);
+  if (a.cols <= 16384) return norm_go<E, OUT, 1024, 2>(a, s);
+  if (a.cols <= 32768) return norm_go<E, OUT, 1024, 4>(a, s);
+  return norm_go<E, OUT, 1024, 0>(a, s);
 }
 
 template <class E>
-void norm_by_out(const NormArgs &a, hipStream_t s) {
-  if (a.out_dtype == HF_F8E4M3) norm_by_length<E, HF_F8E4M3>(a, s);
-  else if (a.out_dtype == HF_S8) norm_by_length<E, HF_S8>(a, s);
-  else norm_by_length<E, -1>(a, s);
+hipError_t norm_by_out(const NormArgs &a, hipStream_t s) {
+  if (a.out_dtype == HF_F8E4M3) return norm_by_length<E, HF_F8E4M3>(a, s);
+  if (a.out_dtype == HF_S8) return norm_by_length<E, HF_S8>(a, s);
+  return norm_by_length<E, -1>(a, s);
 }
 
 template <class E, int T, int NV>
-void norm_grad_go(const NormGradArgs &a, hipStream_t s) {
+hipError_t norm_grad_go(const NormGradArgs &a, hipStream_t s) {
   const int per = T == 64 ? 4 : 1;
-  const unsigned grid = (unsigned)((a.groups + per - 1) / per);
-  const unsigned block = T == 64 ? 256 : T;
-  if (a.vec)
-    norm_grad_kernel<E, T, NV, true><<<grid, block, 0, s>>>(a);
-  else if constexpr (NV < 4)
-    norm_grad_kernel<E, T, NV, false><<<grid, block, 0, s>>>(a);
+  const dim3 grid((unsigned)((a.groups + per - 1) / per));
+  return launch(a.vec ? norm_grad_kernel<E, T, NV, true> : norm_grad_kernel<E, T, NV, false>, grid,
+                T == 64 ? 256 : T, s, a);
+}
+
+// Rows of 8193 to 16384 columns stay in registers where those suffice for
+// them: in 16 bits, with whole vectors (2000 x 16384 bf16: 64 us, read twice
+// 121 us).
+template <class E>
+hipError_t norm_grad_by_length(const NormGradArgs &a, hipStream_t s) {
+  if (a.cols <= 512) return norm_grad_go<E, 64, 1>(a, s);
+  if (a.cols <= 2048) return norm_grad_go<E, 256, 1>(a, s);
+  if (a.cols <= 4096) return norm_grad_go<E, 256, 2>(a, s);
+  if (a.cols <= 8192) return norm_grad_go<E, 1024, 1>(a, s);
+  if constexpr (E::kBytes == 2) {
+    if (a.cols <= 16384 && a.vec) return launch(norm_grad_kernel<E, 512, 4, true>, dim3((unsigned)a.groups), 512, s, a);
+  }
+  return launch(a.vec ? norm_grad_long_kernel<E, true> : norm_grad_long_kernel<E, false>, dim3((unsigned)a.groups), 1024,
+                s, a);
 }
 
 template <class E>
-void norm_grad_by_length(const NormGradArgs &a, hipStream_t s) {
-  if (a.cols <= 512) norm_grad_go<E, 64, 1>(a, s);
-  else if (a.cols <= 2048) norm_grad_go<E, 256, 1>(a, s);
-  else if (a.cols <= 4096) norm_grad_go<E, 256, 2>(a, s);
-  else if (a.cols <= 8192) norm_grad_go<E, 1024, 1>(a, s);
-  else if (a.cols <= 16384 && a.vec && E::kBytes == 2) norm_grad_go<E, E::kBytes == 2 ? 512 : 1024, E::kBytes == 2 ? 4 : 1>(a, s);
-  else if (a.vec) norm_grad_long_kernel<E, true><<<(unsigned)a.groups, 1024, 0, s>>>(a);
-  else norm_grad_long_kernel<E, false><<<(unsigned)a.groups, 1024, 0, s>>>(a);
-}
-
-template <class E>
-void dropout_go(const DropoutArgs &a, hipStream_t s) {
+hipError_t dropout_go(const DropoutArgs &a, hipStream_t s) {
   const int64_t vectors = (a.rows * a.cols + 7) / 8;
-  const unsigned grid = (unsigned)((vectors + 255) / 256);
-  if (a.vec)
-    dropout_kernel<E, true><<<grid, 256, 0, s>>>(a);
-  else
-    dropout_kernel<E, false><<<grid, 256, 0, s>>>(a);
+  return launch(a.vec ? dropout_kernel<E, true> : dropout_kernel<E, false>, dim3((unsigned)((vectors + 255) / 256)), 256,
+                s, a);
 }
 
 template <class E>
-void act_grad_go(const ActGradArgs &a, hipStream_t s) {
+hipError_t act_grad_go(const ActGradArgs &a, hipStream_t s) {
   const int64_t width = a.gated || !a.dz ? (int64_t)a.n : a.lddz;
   const dim3 grid((unsigned)((width + 2047) / 2048), (unsigned)a.groups);
-  if (a.gated && a.vec) act_grad_kernel<E, true, true><<<grid, 256, 0, s>>>(a);
-  else if (a.gated) act_grad_kernel<E, true, false><<<grid, 256, 0, s>>>(a);
-  else if (a.vec) act_grad_kernel<E, false, true><<<grid, 256, 0, s>>>(a);
-  else act_grad_kernel<E, false, false><<<grid, 256, 0, s>>>(a);
+  if (a.gated) return launch(a.vec ? act_grad_kernel<E, true, true> : act_grad_kernel<E, true, false>, grid, 256, s, a);
+  return launch(a.vec ? act_grad_kernel<E, false, true> : act_grad_kernel<E, false, false>, grid, 256, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
-  if (a.dtype == HF_BF16) norm_by_out<BF16>(a, s);
-  else if (a.dtype == HF_F16) norm_by_out<F16>(a, s);
-  else norm_by_out<F32>(a, s);
-  return hipGetLastError();
+  if (a.dtype == HF_BF16) return norm_by_out<BF16>(a, s);
+  if (a.dtype == HF_F16) return norm_by_out<F16>(a, s);
+  return norm_by_out<F32>(a, s);
 }
 
 int norm_grad_groups(int64_t rows, int64_t cols) {
@@ -738,45 +731,39 @@ int norm_grad_groups(int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
-  if (a.dtype == HF_BF16) norm_grad_by_length<BF16>(a, s);
-  else if (a.dtype == HF_F16) norm_grad_by_length<F16>(a, s);
-  else norm_grad_by_length<F32>(a, s);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = a.dtype == HF_BF16  ? norm_grad_by_length<BF16>(a, s)
+                       : a.dtype == HF_F16 ? norm_grad_by_length<F16>(a, s)
+                                           : norm_grad_by_length<F32>(a, s);
   return e != hipSuccess ? e : launch_column_fold(a.partial, a.groups, a.cols, a.dweight, s);
 }
 
 hipError_t launch_column_fold(const float *partial, int groups, int64_t cols, float *out, hipStream_t s) {
-  fold_kernel<<<(unsigned)((cols + 15) / 16), 1024, 0, s>>>(partial, groups, cols, out);
-  return hipGetLastError();
+  return launch(fold_kernel, dim3((unsigned)((cols + 15) / 16)), 1024, s, partial, groups, cols, out);
 }
 
 hipError_t launch_dropout(const DropoutArgs &a, hipStream_t s) {
-  if (a.dtype == HF_BF16) dropout_go<BF16>(a, s);
-  else if (a.dtype == HF_F16) dropout_go<F16>(a, s);
-  else dropout_go<F32>(a, s);
-  return hipGetLastError();
+  if (a.dtype == HF_BF16) return dropout_go<BF16>(a, s);
+  if (a.dtype == HF_F16) return dropout_go<F16>(a, s);
+  return dropout_go<F32>(a, s);
 }
 
 int act_grad_groups(int64_t m, int64_t n) {
-  const int64_t wide = (n + 2047) / 2048;
-  const int64_t most = wide >= 64 ? 64 : 4096 / (wide > 0 ? wide : 1) < 512 ? 4096 / (wide > 0 ? wide : 1) : 512;
+  // 4096 workgroups in all, at most 512 partial rows
+  const int64_t wide = n > 0 ? (n + 2047) / 2048 : 1;
+  const int64_t most = wide >= 64 ? 64 : wide >= 8 ? 4096 / wide : 512;
   return (int)(m < 1 ? 1 : m < most ? m : most);
 }
 
 hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s) {
-  if (a.dtype == HF_BF16) act_grad_go<BF16>(a, s);
-  else act_grad_go<F16>(a, s);
-  return hipGetLastError();
+  return a.dtype == HF_BF16 ? act_grad_go<BF16>(a, s) : act_grad_go<F16>(a, s);
 }
 
 hipError_t launch_pack(const void *src, int64_t ld_src, void *dst, int64_t ld_dst, int64_t rows, int64_t cols,
                        int elem_bytes, hipStream_t s) {
   const dim3 grid((unsigned)((ld_dst + 255) / 256), (unsigned)(rows < 4096 ? rows : 4096));
   if (elem_bytes == 1)
-    pack_kernel<uint8_t><<<grid, 256, 0, s>>>((const uint8_t *)src, ld_src, (uint8_t *)dst, ld_dst, rows, cols);
-  else
-    pack_kernel<uint16_t><<<grid, 256, 0, s>>>((const uint16_t *)src, ld_src, (uint16_t *)dst, ld_dst, rows, cols);
-  return hipGetLastError();
+    return launch(pack_kernel<uint8_t>, grid, 256, s, (const uint8_t *)src, ld_src, (uint8_t *)dst, ld_dst, rows, cols);
+  return launch(pack_kernel<uint16_t>, grid, 256, s, (const uint16_t *)src, ld_src, (uint16_t *)dst, ld_dst, rows, cols);
 }
 
 }  // namespace hf

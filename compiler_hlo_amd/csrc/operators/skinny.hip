@@ -144,10 +144,9 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
 template <class Step, bool GATED>
 hipError_t go(const SkinnyArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)((a.p.n + 15) / 16), (unsigned)a.p.splits);
-  if (a.waves == 16) skinny_kernel<Step, GATED, 16><<<grid, 1024, 0, s>>>(a);
-  else if (a.waves == 8) skinny_kernel<Step, GATED, 8><<<grid, 512, 0, s>>>(a);
-  else skinny_kernel<Step, GATED, 4><<<grid, 256, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = a.waves == 16  ? launch(skinny_kernel<Step, GATED, 16>, grid, 1024, s, a)
+                       : a.waves == 8 ? launch(skinny_kernel<Step, GATED, 8>, grid, 512, s, a)
+                                      : launch(skinny_kernel<Step, GATED, 4>, grid, 256, s, a);
   return e != hipSuccess || a.p.splits == 1 ? e : launch_product_fold(a.p.partial, a.p.splits, a.p.ldp, a.p.e, s);
 }
 

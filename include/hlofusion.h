@@ -399,7 +399,11 @@ hf_status hf_fusion_destroy(hf_fusion *f);
  * and f8e4m3 for the products (gradients: bf16 and f16).  out_dtype: bf16,
  * f16 or f32; for the norm also dtype itself, s8 or f8e4m3.  weight_dtype:
  * dtype or f32.  m, n and k may be 0 (a norm needs n >= 1).  s8 products need
- * k < 2^17, so that their 32-bit sums are exact. */
+ * k < 2^17, so that their 32-bit sums are exact.  Sizes go up to 2^30 (rows of
+ * the row operators and of dropout: below 2^31); arrays may be larger than
+ * 2^31 elements.  f8e4m3 products with a 16-bit result and k > 128 are added
+ * by the 8-bit matrix instructions, whose sums of 128 products are exact to
+ * about 2^-17 of the sum of magnitudes; others to f32's rounding. */
 typedef enum {
   HF_OPERATOR_RMS_NORM = 0,
   HF_OPERATOR_RMS_NORM_GRAD = 1,
