@@ -45,7 +45,7 @@ struct Operand {
 struct Product {
   bool on = false, skinny = false;
   Operand a, b;
-  bool a_by_col = false, b_by_col = false, gated = false;
+  bool gated = false;
   int64_t m = 0, n = 0, k = 0;
   int tile = 0, splits = 1, per_split = 1, waves = 8;
   int64_t tiles_full = 0, part_rows = 0, part_cols = 0;
@@ -143,7 +143,8 @@ Operand operand(hf_operator &op, int64_t rows, int64_t cols, int64_t ld, int64_t
 
 int64_t tiles_of(const Product &p, int64_t tile) { return cdiv(p.m, tile) * cdiv(p.n, p.gated ? tile / 2 : tile); }
 
-// The tile, and how the last tiles are shared: the shortest time by a simple
+// The tile (first .. last: 0 the larger, 1 the smaller), and how the last
+// tiles are shared: the shortest time by a simple
 // account, in microseconds.  A round of tiles (256 of the larger, 512 of the
 // smaller, two a compute unit) takes its stages and an end (sums out, the next
 // tile's first loads in); sharing costs a launch and the partial sums' way to
@@ -154,9 +155,9 @@ int64_t tiles_of(const Product &p, int64_t tile) { return cdiv(p.m, tile) * cdiv
 // 16384 e4m3, 272 large tiles, the last 16 shared by 8 workgroups each, 218
 // (303 unshared); 1024 x 4096 x 4096 small tiles, 41 (large 73); 256 x 4096 x
 // 4096 small tiles shared by 4, 22 (unshared 37).
-double choose_tiles(Product &p, int64_t steps, bool wide) {
+double choose_tiles(Product &p, int64_t steps, int first, int last) {
   double best = 1e300;
-  for (int tile = wide ? 1 : 0; tile < 2; ++tile) {
+  for (int tile = first; tile <= last; ++tile) {
     const int64_t t = tile == 0 ? 256 : 128, slots = tile == 0 ? 256 : 512, all = tiles_of(p, t);
     const double full_stage = tile == 0 ? 1.35 : 0.95, end = tile == 0 ? 6.0 : 3.0;
     const auto stage = [&](int64_t groups) { return groups <= slots / 2 ? (tile == 0 ? 1.1 : 0.6) : full_stage; };
@@ -191,7 +192,7 @@ double choose(const hf_operator_desc &d, Product &p, int64_t elem) {
   // e4m3 widened to 16 bits has no registers to spare for the larger tile or
   // for 16 waves a workgroup
   const bool wide = d.dtype == HF_F8E4M3 && f8_wide(d.out_dtype, p.k);
-  if (!p.a_by_col && !p.b_by_col && p.m <= 8) {
+  if (p.m <= 8) {
     p.skinny = true;
     const int64_t columns = cdiv(p.n, 16), blocks = cdiv(kbytes, 512);
     // As many waves a workgroup as let all workgroups run at once (about 5000
@@ -203,7 +204,7 @@ double choose(const hf_operator_desc &d, Product &p, int64_t elem) {
     p.per_split = (int)cdiv(blocks > 0 ? blocks : 1, s);
     p.splits = blocks > 0 ? (int)cdiv(blocks, p.per_split) : 1;
     best = 4.0 + (double)((p.gated ? 2 : 1) * p.n * kbytes) / 5e6;
-  } else if (!p.a_by_col && !p.b_by_col && p.m <= 64) {
+  } else if (p.m <= 64) {
     p.tile = 2;
     // Shares of the contraction: the shortest time by an account like that of
     // the tiles.  A stage takes its share of the memory's rate, or the latency
@@ -221,19 +222,39 @@ double choose(const hf_operator_desc &d, Product &p, int64_t elem) {
       p.splits = steps > 0 ? (int)cdiv(steps, p.per_split) : 1;
     }
   } else {
-    best = choose_tiles(p, cdiv(p.k, 128 / elem), wide);
-    const int64_t t = p.tile == 0 ? 256 : 128;
-    p.part_rows = p.m < t ? p.m : t;
-    p.part_cols = p.gated ? 2 * std::min(t / 2, up(p.n, 8)) : std::min(t, up(p.n, 8));
+    best = choose_tiles(p, cdiv(p.k, 128 / elem), wide ? 1 : 0, 1);
   }
   return best;
+}
+
+// The same for a gradient's two products, which run in one launch with tiles
+// of one size.
+void choose_gradient(Product &p, Product &q) {
+  p.on = p.m > 0 && p.n > 0;
+  q.on = q.m > 0 && q.n > 0;
+  double best = 1e300;
+  const Product p0 = p, q0 = q;
+  for (int tile = 0; tile < 2; ++tile) {
+    Product x = p0, y = q0;
+    double us = 0.0;
+    if (x.on) us += choose_tiles(x, cdiv(x.k, 64), tile, tile);
+    if (y.on) us += choose_tiles(y, cdiv(y.k, 64), tile, tile);
+    if (us >= best) continue;
+    best = us;
+    p = x;
+    q = y;
+    p.tile = q.tile = tile;
+  }
 }
 
 // The partial sums' place, for what choose() chose.
 void place_partials(hf_operator &op, Product &p) {
   if (!p.on || p.splits == 1) return;
   const bool tiles = !p.skinny && p.tile < 2;
-  const int64_t sums = tiles ? (tiles_of(p, p.tile == 0 ? 256 : 128) - p.tiles_full) * p.part_rows * p.part_cols
+  const int64_t t = p.tile == 0 ? 256 : 128;
+  p.part_rows = std::min(p.m, t);
+  p.part_cols = p.gated ? 2 * std::min(t / 2, up(p.n, 8)) : std::min(t, up(p.n, 8));
+  const int64_t sums = tiles ? (tiles_of(p, t) - p.tiles_full) * p.part_rows * p.part_cols
                              : p.m * p.ldp;
   p.partial_at = take(op, p.splits * sums * 4);
 }
@@ -380,11 +401,8 @@ void plan_product_grad(hf_operator &op) {
   p.a = dz;
   p.a.cols = p.k;
   p.b = w;
-  p.b_by_col = true;
   if (op.dz_at >= 0) p.k = op.lddz;  // whole 16-byte chunks; past `wide`, zeros on both sides
   p.a.cols = p.k;
-  choose(d, p, elem);
-  place_partials(op, p);
   // db [wide, k] = dz^T [wide, m] a [m, k]
   Product &q = op.p2;
   q.m = wide;
@@ -394,8 +412,8 @@ void plan_product_grad(hf_operator &op) {
   // whole chunks in the last row too: dz's padding is there to be read
   q.a.cols = up(wide, 8);
   q.b = a;
-  q.a_by_col = q.b_by_col = true;
-  choose(d, q, elem);
+  choose_gradient(p, q);
+  place_partials(op, p);
   place_partials(op, q);
 }
 
@@ -503,10 +521,12 @@ hipError_t place(const Call &c, const Operand &o, const void *src, int64_t elem,
   return launch_pack(src, o.src_ld, dst, o.ld, o.rows, o.src_cols, (int)elem, c.stream);
 }
 
-hipError_t run_product(const Call &c, const Product &p, const void *a, const void *b, int64_t elem, const Epilogue &e) {
-  if (!p.on) return hipSuccess;
-  SkinnyArgs s{};
-  ProductArgs &g = s.p;
+ProductArgs args_of(const Call &c, const Product &p, const void *a, const void *b, int64_t elem, const Epilogue &e) {
+  ProductArgs g{};
+  g.dtype = c.op->d.dtype;
+  g.tile = p.tile;
+  g.splits = 1;
+  if (!p.on) return g;
   g.a = a;
   g.b = b;
   g.lda = p.a.ld * elem;
@@ -517,10 +537,6 @@ hipError_t run_product(const Call &c, const Product &p, const void *a, const voi
   g.m = (int)p.m;
   g.n = (int)p.n;
   g.k = (int)p.k;
-  g.dtype = c.op->d.dtype;
-  g.a_by_col = p.a_by_col;
-  g.b_by_col = p.b_by_col;
-  g.tile = p.tile;
   g.tiles_full = (int)p.tiles_full;
   g.part_rows = (int)p.part_rows;
   g.part_cols = (int)p.part_cols;
@@ -529,9 +545,18 @@ hipError_t run_product(const Call &c, const Product &p, const void *a, const voi
   g.partial = p.splits > 1 ? (float *)(c.ws + p.partial_at) : nullptr;
   g.ldp = p.ldp;
   g.e = e;
+  return g;
+}
+
+hipError_t run_product(const Call &c, const Product &p, const void *a, const void *b, int64_t elem, const Epilogue &e) {
+  if (!p.on) return hipSuccess;
+  const ProductArgs g = args_of(c, p, a, b, elem, e);
+  if (!p.skinny) return launch_product(g, c.stream);
+  SkinnyArgs s{};
+  s.p = g;
   s.waves = p.waves;
   s.blocks_per_split = p.per_split;
-  return p.skinny ? launch_skinny(s, c.stream) : launch_product(g, c.stream);
+  return launch_skinny(s, c.stream);
 }
 
 hipError_t run_norm(const Call &c) {
@@ -667,8 +692,8 @@ hipError_t run_product_grad(const Call &c) {
     e.vec = op.buf[i].rows <= 1 || op.buf[i].ld % 8 == 0;
     return e;
   };
-  HF_TRY(run_product(c, op.p1, dz, b, 2, plain(op.n_params, op.p1)));
-  return run_product(c, op.p2, dz, a, 2, plain(op.n_params + 1, op.p2));
+  return launch_gradient(args_of(c, op.p1, dz, b, 2, plain(op.n_params, op.p1)),
+                         args_of(c, op.p2, dz, a, 2, plain(op.n_params + 1, op.p2)), c.stream);
 }
 
 // Two buffers that share no element.  Column windows of one array (equal row

@@ -94,7 +94,6 @@ struct ProductArgs {
   int64_t b_half;            // gated: bytes from a gate row to its up row
   int32_t m, n, k;           // n: columns of d (gated: of one half); k: elements
   int32_t dtype;
-  bool a_by_col, b_by_col;   // the contraction runs over the operand's rows
   int32_t tile;              // 0: 256 x 256, 1: 128 x 128 (columns of the product), 2: strips, m <= 64 by row
   int32_t tiles_full;        // tiles 0 and 1: so many are one workgroup's, the others `splits` workgroups'
   int32_t splits, k_tiles_per_split;
@@ -106,6 +105,10 @@ struct ProductArgs {
   Epilogue e;
 };
 hipError_t launch_product(const ProductArgs &a, hipStream_t s);
+// da = dz b (the contraction runs over b's rows) and db = dz^T a (over both
+// operands' rows), tiles of one size; one of them may be empty (m or n 0,
+// tiles_full 0, splits 1).
+hipError_t launch_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t s);
 // Which e4m3 products go through f16 (StepF8Wide).
 constexpr bool f8_wide(int out_dtype, int64_t k) { return out_dtype == HF_F32 || k <= 128; }
 

@@ -157,18 +157,23 @@ __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &t
 // 128 x 128 with 4 waves, two of them.  A wave has HM/2 x 32 sums in each
 // quarter of the tile; gated, the second half of the columns is the up half
 // of the first, so a lane holds gate and up of the same element.
+template <int HM, int HN>
+struct Shape {
+  static constexpr int kWaves = 2 * (HN / 32), kThreads = kWaves * 64;
+  static constexpr int kStage = 256 * (HM + HN);
+  // the sums on their way out: rows of 2 HN with a pad of 16 bytes
+  static constexpr int kPitch = 2 * HN + 4, kOut = HM * kPitch * 4;
+  static constexpr int kLds = 2 * kStage > kOut ? 2 * kStage : kOut;
+};
+
 template <class Step, bool ACOL, bool BCOL, int HM, int HN>
-__global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void product_kernel(ProductArgs a) {
-  constexpr int WN = HN / 32, WAVES = 2 * WN, THREADS = WAVES * 64;
+__device__ __forceinline__ void product_tile(const ProductArgs &a, int block, char *lds) {
+  typedef Shape<HM, HN> S;
+  constexpr int WN = HN / 32, WAVES = S::kWaves, THREADS = S::kThreads, kStage = S::kStage, kPitch = S::kPitch;
   typedef Half<HM, ACOL, WAVES> HA;
   typedef Half<HN, BCOL, WAVES> HB;
   constexpr int TM = HM / 32, TN = 2;  // 16 x 16 tiles of a wave in a quarter
-  constexpr int kStage = 2 * HA::kBytes + 2 * HB::kBytes;
-  // the stages, then rows of 2 HN sums with a pad of 16 bytes (Out)
-  constexpr int kPitch = 2 * HN + 4;
-  constexpr int kOut = HM * kPitch * 4;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage > kOut ? 2 * kStage : kOut];
-  char *lds0 = lds, *lds1 = lds + kStage;
+  static_assert(kStage == 2 * HA::kBytes + 2 * HB::kBytes, "two halves of both operands");
 
   const bool gated = a.e.gated;
   const int tile_n = gated ? HN : 2 * HN;
@@ -177,11 +182,11 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void product_kernel(Produ
   // leave most of the chip idle for a whole tile's time, are shared by
   // `splits` workgroups each, one part of the contraction a workgroup.
   const int tiles = tiles_m * tiles_n, rest = tiles - a.tiles_full;
-  const bool part = (int)blockIdx.x >= a.tiles_full;
+  const bool part = block >= a.tiles_full;
   // Consecutive workgroups go to different XCDs; each XCD takes a contiguous
   // run of tiles, in columns of 4 tile rows, so that the tiles it works on at
   // a time share rows and columns in its L2.
-  int id = part ? blockIdx.x - a.tiles_full : blockIdx.x;
+  int id = part ? block - a.tiles_full : block;
   {
     const int count = part ? rest * a.splits : a.tiles_full;
     const int xcd = id % 8, q = count / 8, r = count % 8;
@@ -369,6 +374,24 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void product_kernel(Produ
   }
 }
 
+template <class Step, int HM, int HN>
+__global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void product_kernel(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<HM, HN>::kLds];
+  product_tile<Step, false, false, HM, HN>(a, blockIdx.x, lds);
+}
+
+// The two products of a gradient, da = dz b and db = dz^T a, in one launch:
+// neither needs the other, small ones fill the chip together and large ones
+// share their last round.
+template <class Step, int HM, int HN>
+__global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void gradient_kernel(ProductArgs da, ProductArgs db, int first) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<HM, HN>::kLds];
+  if ((int)blockIdx.x < first)
+    product_tile<Step, false, true, HM, HN>(da, blockIdx.x, lds);
+  else
+    product_tile<Step, true, true, HM, HN>(db, blockIdx.x - first, lds);
+}
+
 // The product for up to 64 rows, bound by reading b: a strip of 256 columns
 // (gated: 128 and their up half) a workgroup of 8 waves, 16 columns of each
 // half a wave, all rows.  Both operands go through LDS in whole 128-byte
@@ -507,15 +530,14 @@ __global__ __launch_bounds__(256) void product_fold_kernel(const float *partial,
   }
 }
 
-// The same for the shared tiles of product_kernel: 1/8 of a tile's rows a
-// workgroup.
-__global__ __launch_bounds__(256) void product_tile_fold_kernel(ProductArgs a, int size) {
+// The same for the shared tiles: 1/8 of a tile's rows a workgroup.
+__device__ __forceinline__ void fold_tile(const ProductArgs &a, int size, int block) {
   const bool gated = a.e.gated;
   const int tile_n = gated ? size / 2 : size, per = tile_n / 8;
   const int tiles_m = (a.m + size - 1) / size, tiles_n = (a.n + tile_n - 1) / tile_n;
   const int rest = tiles_m * tiles_n - a.tiles_full;
   int tm, tn;
-  tile_at(a.tiles_full + blockIdx.x, tiles_m, tiles_n, tm, tn);
+  tile_at(a.tiles_full + block, tiles_m, tiles_n, tm, tn);
   for (int at = threadIdx.x; at < size / 8 * per; at += 256) {
     const int r = blockIdx.y * (size / 8) + at / per, c = at % per * 8, m = tm * size + r, n = tn * tile_n + c;
     if (m >= a.m || n >= a.n) continue;
@@ -523,7 +545,7 @@ __global__ __launch_bounds__(256) void product_tile_fold_kernel(ProductArgs a, i
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
     for (int s = 0; s < a.splits; ++s) {
-      const float *p = a.partial + (((int64_t)s * rest + blockIdx.x) * a.part_rows + r) * a.part_cols + c;
+      const float *p = a.partial + (((int64_t)s * rest + block) * a.part_rows + r) * a.part_cols + c;
       load8<F32>(p, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += x[i];
@@ -537,19 +559,45 @@ __global__ __launch_bounds__(256) void product_tile_fold_kernel(ProductArgs a, i
   }
 }
 
-template <class Step, bool ACOL, bool BCOL>
-hipError_t go(const ProductArgs &a, hipStream_t s) {
+__global__ __launch_bounds__(256) void product_tile_fold_kernel(ProductArgs a, ProductArgs b, int first, int size) {
+  if ((int)blockIdx.x < first)
+    fold_tile(a, size, blockIdx.x);
+  else
+    fold_tile(b, size, blockIdx.x - first);
+}
+
+// The tiles that are shared by workgroups, and the workgroups of a product.
+int64_t shared_tiles(const ProductArgs &a) {
   const int64_t tile = a.tile == 0 ? 256 : 128, tile_n = a.e.gated ? tile / 2 : tile;
-  const int64_t rest = ((a.m + tile - 1) / tile) * ((a.n + tile_n - 1) / tile_n) - a.tiles_full;
-  const unsigned grid = (unsigned)(a.tiles_full + rest * a.splits);
+  return ((a.m + tile - 1) / tile) * ((a.n + tile_n - 1) / tile_n) - a.tiles_full;
+}
+unsigned groups_of(const ProductArgs &a) { return (unsigned)(a.tiles_full + shared_tiles(a) * a.splits); }
+
+// b may be empty (m = 0)
+hipError_t fold_shared(const ProductArgs &a, const ProductArgs &b, hipStream_t s) {
+  const int64_t x = a.splits > 1 ? shared_tiles(a) : 0, y = b.splits > 1 ? shared_tiles(b) : 0;
+  if (x + y == 0) return hipSuccess;
+  return launch(product_tile_fold_kernel, dim3((unsigned)(x + y), 8), 256, s, a, b, (int)x, a.tile == 0 ? 256 : 128);
+}
+
+template <class Step>
+hipError_t go(const ProductArgs &a, hipStream_t s) {
   hipError_t e = hipErrorInvalidValue;
   if (a.tile == 1) {
-    e = launch(product_kernel<Step, ACOL, BCOL, 64, 64>, grid, 256, s, a);
+    e = launch(product_kernel<Step, 64, 64>, dim3(groups_of(a)), 256, s, a);
   } else if constexpr (!Step::kWide) {  // never planned with kWide
-    e = launch(product_kernel<Step, ACOL, BCOL, 128, 128>, grid, 512, s, a);
+    e = launch(product_kernel<Step, 128, 128>, dim3(groups_of(a)), 512, s, a);
   }
-  if (e != hipSuccess || rest == 0 || a.splits == 1) return e;
-  return launch(product_tile_fold_kernel, dim3((unsigned)rest, 8), 256, s, a, (int)tile);
+  return e != hipSuccess ? e : fold_shared(a, ProductArgs{}, s);
+}
+
+template <class Step>
+hipError_t go_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t s) {
+  const unsigned x = groups_of(da), y = groups_of(db);
+  if (x + y == 0) return hipSuccess;
+  const hipError_t e = da.tile == 0 ? launch(gradient_kernel<Step, 128, 128>, dim3(x + y), 512, s, da, db, (int)x)
+                                    : launch(gradient_kernel<Step, 64, 64>, dim3(x + y), 256, s, da, db, (int)x);
+  return e != hipSuccess ? e : fold_shared(da, db, s);
 }
 
 template <class Step>
@@ -561,24 +609,21 @@ hipError_t go_strip(const ProductArgs &a, hipStream_t s) {
 }
 
 template <class Step>
-hipError_t by_layout(const ProductArgs &a, hipStream_t s) {
-  if (a.tile == 2) return go_strip<Step>(a, s);
-  if (!a.a_by_col && !a.b_by_col) return go<Step, false, false>(a, s);
-  if constexpr (Step::kBytes == 2) {
-    if (!a.a_by_col) return go<Step, false, true>(a, s);
-    if (a.b_by_col) return go<Step, true, true>(a, s);
-  }
-  return hipErrorInvalidValue;  // not planned: only 16-bit gradients run over rows
+hipError_t either(const ProductArgs &a, hipStream_t s) {
+  return a.tile == 2 ? go_strip<Step>(a, s) : go<Step>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_product(const ProductArgs &a, hipStream_t s) {
-  if (a.dtype == HF_BF16) return by_layout<StepBF16>(a, s);
-  if (a.dtype == HF_F16) return by_layout<StepF16>(a, s);
-  if (a.dtype == HF_F8E4M3)
-    return f8_wide(a.e.out_dtype, a.k) ? by_layout<StepF8Wide>(a, s) : by_layout<StepF8>(a, s);
-  return by_layout<StepS8>(a, s);
+  if (a.dtype == HF_BF16) return either<StepBF16>(a, s);
+  if (a.dtype == HF_F16) return either<StepF16>(a, s);
+  if (a.dtype == HF_F8E4M3) return f8_wide(a.e.out_dtype, a.k) ? either<StepF8Wide>(a, s) : either<StepF8>(a, s);
+  return either<StepS8>(a, s);
+}
+
+hipError_t launch_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t s) {
+  return da.dtype == HF_BF16 ? go_gradient<StepBF16>(da, db, s) : go_gradient<StepF16>(da, db, s);
 }
 
 hipError_t launch_product_fold(const float *partial, int splits, int64_t ldp, const Epilogue &e, hipStream_t s) {
