@@ -205,3 +205,21 @@ def test_workspace_is_bounded_by_the_operands():
         packed = 2 * (pad(n) * m + pad(k) * (m + n)) + 4 * 512 * n
         partial = 16 * 4 * (m * pad(k) + n * pad(k))
         assert ws <= packed + partial + 4096
+
+
+@pytest.mark.parametrize("m, n, k, dtype, want", [
+    (1, 4096, 16384, "bf16", (16, 16, 1)),     # few rows: registers, 256 column groups of 16 waves
+    (8, 512, 16384, "bf16", (16, 16, 4)),      # too few column groups: the contraction over workgroups too
+    (9, 4096, 4096, "bf16", (64, 256, 8)),     # strips
+    (64, 22528, 4096, "bf16", (64, 256, 2)),
+    (65, 64, 64, "bf16", (128, 128, 1)),       # tiles
+    (1024, 4096, 4096, "bf16", (128, 128, 1)),
+    (256, 4096, 4096, "bf16", (128, 128, 4)),  # shared by 4 workgroups
+    (8192, 8192, 8192, "bf16", (256, 256, 1)),
+    (4096, 4096, 16384, "f8e4m3", (256, 256, 1)),
+])
+def test_tile_and_split_choices(m, n, k, dtype, want):
+    """The kernels chosen for shapes that were measured."""
+    p = H.Matmul(m, n, k, dtype, mode="plan").plan()
+    assert (p["tile_rows"], p["tile_cols"], p["splits"]) == want
+    assert (p["workspace_bytes"] > 0) == (want[2] > 1)
