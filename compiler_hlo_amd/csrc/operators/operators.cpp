@@ -192,28 +192,34 @@ double choose(const hf_operator_desc &d, Product &p, int64_t elem) {
   // e4m3 widened to 16 bits has no registers to spare for the larger tile or
   // for 16 waves a workgroup
   const bool wide = d.dtype == HF_F8E4M3 && f8_wide(d.out_dtype, p.k);
-  if (p.m <= 8) {
+  const int64_t strips = cdiv(p.n, p.gated ? 64 : 128);
+  if (p.m <= 8 && strips <= 64) {
+    // Too few strips to fill the chip without sharing the contraction, and so
+    // few rows that reading them once for every 16 columns costs little (1 x
+    // 4096 x 16384 bf16 26 us, strips 30; 8 x 4096 x 4096 10, strips 12).  With
+    // more columns strips are as fast or faster (1 x 22528 x 4096 34 us, skinny
+    // 36; 8 rows 34.5 and 43).
     p.skinny = true;
     const int64_t columns = cdiv(p.n, 16), blocks = cdiv(kbytes, 512);
     // As many waves a workgroup as let all workgroups run at once (about 5000
     // waves fit): a second round of workgroups for the last few costs as much
     // as the first.
-    p.waves = columns * 16 <= 5120 && !wide ? 16 : columns * 8 <= 5120 ? 8 : 4;
+    p.waves = columns * 16 <= 5120 && !wide ? 16 : 8;
     int64_t s = 1;
     while (columns * s < 256 && blocks >= 2 * s * p.waves) s *= 2;
     p.per_split = (int)cdiv(blocks > 0 ? blocks : 1, s);
     p.splits = blocks > 0 ? (int)cdiv(blocks, p.per_split) : 1;
     best = 4.0 + (double)((p.gated ? 2 : 1) * p.n * kbytes) / 5e6;
   } else if (p.m <= 64) {
-    p.tile = 2;
     // Shares of the contraction: the shortest time by an account like that of
     // the tiles.  A stage takes its share of the memory's rate, or the latency
-    // that two stages in flight leave where there are few workgroups (fits to
-    // 16 .. 64 rows; 24 x 22528 x 4096 by 2: 41 us, unshared 52; 64 x 4096 x
-    // 4096 by 8: 16 us, unshared 42, by 16 21).
-    const int64_t strips = cdiv(p.n, p.gated ? 128 : 256), steps = cdiv(p.k, 128 / elem);
+    // that four stages in flight leave where there are few workgroups (fits to
+    // 16 .. 64 rows, within 20%: 64 x 4096 x 4096 by 4 16 us, unshared 30; 32 x
+    // 4096 x 16384 by 8 32 us, unshared 96; 24 x 22528 x 4096 unshared 38).
+    p.tile = 2;
+    const int64_t steps = cdiv(p.k, 128 / elem);
     for (int64_t s = 1; s <= 32 && (s == 1 || (strips * s <= 256 && steps >= 2 * s)); ++s) {
-      const double stage = std::max(0.6 + 0.0035 * (double)p.m, 0.0065 * (double)std::min<int64_t>(strips * s, 256));
+      const double stage = std::max(0.25 + 0.003 * (double)p.m, 0.00325 * (double)std::min<int64_t>(strips * s, 256));
       double us = (double)cdiv(strips * s, 256) * ((double)cdiv(steps, s) * stage + 3.0);
       if (s > 1) us += 3.5 + 8.0 * (double)(s * p.m * p.ldp) / 5e6;
       if (us >= best) continue;
@@ -488,7 +494,7 @@ void make_plan(hf_operator &op) {
     f.algorithmic_flops = (grad ? 4 : 2) * d.m * wide * d.k;
     if (op.p1.on) {
       f.tile_rows = op.p1.skinny ? 16 : op.p1.tile == 0 ? 256 : op.p1.tile == 1 ? 128 : 64;
-      f.tile_cols = op.p1.skinny ? (op.p1.gated ? 32 : 16) : op.p1.tile == 1 ? 128 : 256;
+      f.tile_cols = op.p1.skinny ? (op.p1.gated ? 32 : 16) : op.p1.tile == 0 ? 256 : 128;
       f.splits = op.p1.splits;
     }
   }

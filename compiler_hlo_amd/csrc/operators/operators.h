@@ -94,7 +94,7 @@ struct ProductArgs {
   int64_t b_half;            // gated: bytes from a gate row to its up row
   int32_t m, n, k;           // n: columns of d (gated: of one half); k: elements
   int32_t dtype;
-  int32_t tile;              // 0: 256 x 256, 1: 128 x 128 (columns of the product), 2: strips, m <= 64 by row
+  int32_t tile;              // 0: 256 x 256, 1: 128 x 128 (columns of the product), 2: strips, m <= 64
   int32_t tiles_full;        // tiles 0 and 1: so many are one workgroup's, the others `splits` workgroups'
   int32_t splits, k_tiles_per_split;
   // splits > 1: [splits][shared tiles][part_rows][part_cols], the up half's
@@ -114,7 +114,7 @@ constexpr bool f8_wide(int out_dtype, int64_t k) { return out_dtype == HF_F32 ||
 
 struct SkinnyArgs {
   ProductArgs p;             // splits: workgroups over k
-  int32_t waves;             // of a workgroup: 4, 8 or 16
+  int32_t waves;             // of a workgroup: 8 or 16
   int32_t blocks_per_split;  // blocks of 512 contraction bytes
 };
 

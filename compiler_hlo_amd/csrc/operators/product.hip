@@ -397,26 +397,27 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void gradient_kernel(Prod
     product_tile<Step, true, true, HM, HN>(db, blockIdx.x - first, lds);
 }
 
-// The product for up to 64 rows, bound by reading b: a strip of 256 columns
-// (gated: 128 and their up half) a workgroup of 8 waves, 16 columns of each
-// half a wave, all rows.  Both operands go through LDS in whole 128-byte
-// lines, a once for 256 columns.  Three stages of 40 KiB, two of them in
-// flight: more than the memory's latency times its rate a compute unit needs.
-// 24 x 22528 x 4096 gated bf16 takes 41.6 us (4.5 TB/s) with the fold of its
-// two shares, and 64 rows 48; from registers, as the skinny product does it,
-// 51 and 75.
+// The product for up to 64 rows, bound by reading b: a strip of 128 columns
+// (gated: 64 and their up half) a workgroup of 8 waves, 16 columns a wave, all
+// rows.  Both operands go through LDS in whole 128-byte lines, a once for 128
+// columns.  Five stages of 24 KiB, four of them in flight: twice what the
+// memory's latency times its rate a compute unit needs.  24 x 22528 x 4096
+// gated bf16 takes 37 us (5.0 TB/s), 64 rows 42; with strips of 256 columns,
+// which have to share the contraction of such a layer to fill the chip, 41 and
+// 47; from registers, as the skinny product does it, 51 and 75.
 template <class Step>
 __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
+  constexpr int HN = 64;
   typedef Half<64, false, 8> HA;
-  typedef Half<128, false, 8> HB;
-  constexpr int TM = 4;
-  constexpr int kStage = HA::kBytes + 2 * HB::kBytes, kStages = 3;
-  constexpr int kPitch = 256 + 4;
+  typedef Half<HN, false, 8> HB;
+  constexpr int TM = 4;  // 16 x 16 tiles of a wave
+  constexpr int kStage = HA::kBytes + 2 * HB::kBytes, kStages = 5;
+  constexpr int kPitch = 2 * HN + 4;
   __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
   static_assert(64 * kPitch * 4 <= kStages * kStage, "the sums go out through the stages");
 
   const bool gated = a.e.gated;
-  const int width = gated ? 128 : 256;
+  const int width = gated ? HN : 2 * HN;
   const int n0 = blockIdx.x * width;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
   constexpr int kStep = 128 / Step::kBytes;
@@ -425,7 +426,7 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
   const int kn = all - k0 < a.k_tiles_per_split ? all - k0 : a.k_tiles_per_split;
   const int left = (k0 + kn) * kStep < a.k ? kn * 128 : (a.k - k0 * kStep) * Step::kBytes;
   const int64_t a0 = (int64_t)k0 * 128, b0 = (int64_t)n0 * a.ldb + (int64_t)k0 * 128;
-  const int64_t b_half = gated ? a.b_half : 128 * a.ldb;
+  const int64_t b_half = gated ? a.b_half : HN * a.ldb;
   const i32x4 ra = view((const char *)a.a + a0, a.a_bytes - a0);
   const i32x4 rb[2] = {view((const char *)a.b + b0, a.b_bytes - b0),
                        view((const char *)a.b + b0 + b_half, a.b_bytes - b0 - b_half)};
@@ -445,46 +446,39 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) HB::load(to + HA::kBytes + h * HB::kBytes, rb[h], vb, t * 128, past);
   };
-  typename Step::Acc acc[2][TM];
+  typename Step::Acc acc[TM];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int x = 0; x < TM; ++x) acc[j][x] = typename Step::Acc{0, 0, 0, 0};
+  for (int x = 0; x < TM; ++x) acc[x] = typename Step::Acc{0, 0, 0, 0};
+  const int half = w / 4, col = (w % 4) * 16;  // this wave's columns
   uint32_t pa[2], pb[2];
   HA::addresses<TM>(base, 0, pa);
-  HB::addresses<1>(base + HA::kBytes, w * 16, pb);
+  HB::addresses<1>(base + HA::kBytes + half * HB::kBytes, col, pb);
   auto add = [&](int stage) {
     const uint32_t at = stage * kStage;
-    i32x4 fb[2][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) HB::read<1>(pb, at + j * HB::kBytes, 0, fb[j]);
+    i32x4 fb[2];
+    HB::read<1>(pb, at, 0, fb);
 #pragma unroll
     for (int x = 0; x < TM; ++x) {
       if (x * 16 >= a.m) break;
       i32x4 fa[2];
       HA::read<TM>(pa, at, x, fa);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[j][x] = mma<Step>(fa, fb[j], acc[j][x]);
+      acc[x] = mma<Step>(fa, fb, acc[x]);
     }
   };
-  // A stage's loads have arrived when only the next stage's are left; after
-  // the barrier every wave's have, and every wave is done with the stage
-  // before it, whose place the stage after the next then takes.
+  // A stage's loads have arrived when only those of the stages after it are
+  // left; after the barrier every wave's have, and every wave is done with the
+  // stage before it, whose place the newest stage then takes.
   constexpr int kLoads = HA::kLoads + 2 * HB::kLoads;
   if (kn > 0) {
-    fetch(0, 0);
-    fetch(1, 1);
-    for (int kt = 0; kt < kn; kt += 3) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        arrived<kLoads>();
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
+    for (int kt = 0; kt < kn; kt += kStages) {
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) {
+        arrived<kLoads *(kStages - 2)>();
         meet();
-        if (kt + i < kn) {
-          fetch(kt + i + 2, (i + 2) % 3);
-          add(i);
-        } else {
-          fetch(kn, (i + 2) % 3);
-        }
+        fetch(kt + i + kStages - 1, (i + kStages - 1) % kStages);
+        if (kt + i < kn) add(i);
       }
     }
     arrived<0>();
@@ -493,9 +487,7 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
   __syncthreads();
 #pragma unroll
   for (int x = 0; x < TM; ++x)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *(f32x4 *)(out + (x * 16 + (l & 15)) * kPitch + j * 128 + w * 16 + (l >> 4) * 4) = Step::sums(acc[j][x]);
+    *(f32x4 *)(out + (x * 16 + (l & 15)) * kPitch + half * HN + col + (l >> 4) * 4) = Step::sums(acc[x]);
   __syncthreads();
   const int per = width / 8;
 #pragma unroll 1
@@ -504,7 +496,7 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
     if (n >= a.n) continue;
     float v[8], u[8];
     load8<F32>(out + m * kPitch + c, v);
-    if (gated) load8<F32>(out + m * kPitch + 128 + c, u);
+    if (gated) load8<F32>(out + m * kPitch + HN + c, u);
     if (a.splits > 1) {
       float *p = a.partial + ((int64_t)blockIdx.y * a.m + m) * a.ldp + n;
       store8<F32>(p, v);
@@ -610,7 +602,7 @@ hipError_t go_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t
 
 template <class Step>
 hipError_t go_strip(const ProductArgs &a, hipStream_t s) {
-  const int width = a.e.gated ? 128 : 256;
+  const int width = a.e.gated ? 64 : 128;
   const dim3 grid((unsigned)((a.n + width - 1) / width), (unsigned)a.splits);
   const hipError_t e = launch(strip_kernel<Step>, grid, 512, s, a);
   return e != hipSuccess || a.splits == 1 ? e : launch_product_fold(a.partial, a.splits, a.ldp, a.e, s);

@@ -13,8 +13,8 @@ namespace {
 // them: a lane reads 16 bytes of one row, 4 lanes 64 bytes of it, and the next
 // load the next 64.  b is read once by the whole launch; a comes from L2, once
 // for every 16 columns, which is why more than 8 rows are the strips' (there a
-// is read once for 256 columns): 16 x 22528 x 4096 bf16 takes 52 us here and
-// 39 us there, 1 x 4096 x 16384 26 us here (5.2 TB/s) and 32 us there.
+// is read once for 128 columns): 16 x 4096 x 16384 bf16 takes 36 us here and
+// 32 us there, 1 row 26 us here (5.2 TB/s) and 30 us there.
 template <class Step, bool GATED, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
   const ProductArgs &a = s.p;
@@ -144,9 +144,12 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
 template <class Step, bool GATED>
 hipError_t go(const SkinnyArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)((a.p.n + 15) / 16), (unsigned)a.p.splits);
-  const hipError_t e = a.waves == 16  ? launch(skinny_kernel<Step, GATED, 16>, grid, 1024, s, a)
-                       : a.waves == 8 ? launch(skinny_kernel<Step, GATED, 8>, grid, 512, s, a)
-                                      : launch(skinny_kernel<Step, GATED, 4>, grid, 256, s, a);
+  hipError_t e = hipErrorInvalidValue;
+  if (a.waves == 8) {
+    e = launch(skinny_kernel<Step, GATED, 8>, grid, 512, s, a);
+  } else if constexpr (!Step::kWide) {  // never planned with kWide
+    e = launch(skinny_kernel<Step, GATED, 16>, grid, 1024, s, a);
+  }
   return e != hipSuccess || a.p.splits == 1 ? e : launch_product_fold(a.p.partial, a.p.splits, a.p.ldp, a.p.e, s);
 }
 

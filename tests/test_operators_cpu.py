@@ -210,8 +210,9 @@ def test_workspace_is_bounded_by_the_operands():
 @pytest.mark.parametrize("m, n, k, dtype, want", [
     (1, 4096, 16384, "bf16", (16, 16, 1)),     # few rows: registers, 256 column groups of 16 waves
     (8, 512, 16384, "bf16", (16, 16, 4)),      # too few column groups: the contraction over workgroups too
-    (9, 4096, 4096, "bf16", (64, 256, 8)),     # strips
-    (64, 22528, 4096, "bf16", (64, 256, 2)),
+    (9, 4096, 4096, "bf16", (64, 128, 4)),     # strips, shared by 4 workgroups
+    (64, 22528, 4096, "bf16", (64, 128, 1)),
+    (1, 22528, 4096, "bf16", (64, 128, 1)),    # enough columns for strips from one row on
     (65, 64, 64, "bf16", (128, 128, 1)),       # tiles
     (1024, 4096, 4096, "bf16", (128, 128, 1)),
     (256, 4096, 4096, "bf16", (128, 128, 4)),  # shared by 4 workgroups

@@ -772,3 +772,23 @@ def test_gated_last_rows():
     R.close(zs, z, err, torch.float16)
     f, u = R.act("relu", z[:, :n])[0], z[:, n:]
     R.close(d, f * u, err[:, :n] * (u.abs() + err[:, n:]) + f.abs() * err[:, n:] + (f * u).abs() * 2.0 ** -24, torch.float16)
+
+
+@pytest.mark.parametrize("m, n, k", [(1, 8500, 384), (7, 8400, 1000), (33, 8330, 72), (64, 20000, 264), (9, 40, 4096)])
+def test_strips(m, n, k):
+    """Many columns take strips from one row on; more strips than compute
+    units; a few columns shared by many workgroups."""
+    for dtype, out in (("bf16", "bf16"), ("s8", "f32"), ("f8e4m3", "f16")):
+        say("strips", dtype, m, n, k, H.Matmul(m, n, k, dtype, out_dtype=out, mode="plan").plan())
+        g = gen(m + n)
+        ops = operands(g, m, n, k, dtype)
+        extra = {"bias": normal(g, (n,), out)}
+        op = H.Matmul(m, n, k, dtype, out_dtype=out, bias=True, activation="relu")
+        check_matmul(ops, extra, op(*ops, *extra.values()), out, "relu", False)
+    gops = operands(gen(m), m, 2 * (n // 2), k, "f16")
+    z, mag = sums(gops)
+    err, half = R.sum_error(mag, k) + 4 * 2.0 ** -24 * mag, n // 2
+    d = H.GatedFeedForward(m, half, k, "f16", out_dtype="f32", activation="relu")(*gops)
+    f, u = R.act("relu", z[:, :half])[0], z[:, half:]
+    R.close(d, f * u, err[:, :half] * (u.abs() + err[:, half:]) + f.abs() * err[:, half:] + (f * u).abs() * 2.0 ** -24,
+            torch.float32)
