@@ -347,7 +347,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   // four sums are 16 bytes; the pad keeps neighbouring rows in different banks.
   const int l = threadIdx.x % 64;
   float *out = (float *)lds;
-  const int per = tile_n / 8;  // threads a row
+  const int shift = __builtin_ctz(tile_n / 8), per = 1 << shift;  // threads a row
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     __syncthreads();
@@ -362,7 +362,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
     __syncthreads();
 #pragma unroll 1
     for (int at = threadIdx.x; at < HM * per; at += THREADS) {
-      const int r = at / per, c = at % per * 8, m = m0 + i * HM + r, n = n0 + c;
+      const int r = at >> shift, c = (at & (per - 1)) * 8, m = m0 + i * HM + r, n = n0 + c;
       float v[8], u[8];
       load8<F32>(out + r * kPitch + c, v);
       if (gated) load8<F32>(out + r * kPitch + HN + c, u);
@@ -489,10 +489,10 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
   for (int x = 0; x < TM; ++x)
     *(f32x4 *)(out + (x * 16 + (l & 15)) * kPitch + half * HN + col + (l >> 4) * 4) = Step::sums(acc[x]);
   __syncthreads();
-  const int per = width / 8;
+  const int shift = __builtin_ctz(width / 8), per = 1 << shift;
 #pragma unroll 1
   for (int at = threadIdx.x; at < a.m * per; at += 512) {
-    const int m = at / per, c = at % per * 8, n = n0 + c;
+    const int m = at >> shift, c = (at & (per - 1)) * 8, n = n0 + c;
     if (n >= a.n) continue;
     float v[8], u[8];
     load8<F32>(out + m * kPitch + c, v);
@@ -533,13 +533,13 @@ __global__ __launch_bounds__(256) void product_fold_kernel(const float *partial,
 // The same for the shared tiles: 1/8 of a tile's rows a workgroup.
 __device__ __forceinline__ void fold_tile(const ProductArgs &a, int size, int block) {
   const bool gated = a.e.gated;
-  const int tile_n = gated ? size / 2 : size, per = tile_n / 8;
+  const int tile_n = gated ? size / 2 : size, shift = __builtin_ctz(tile_n / 8), per = 1 << shift;
   const int tiles_m = (a.m + size - 1) / size, tiles_n = (a.n + tile_n - 1) / tile_n;
   const int rest = tiles_m * tiles_n - a.tiles_full;
   int tm, tn;
   tile_at(a.tiles_full + block, tiles_m, tiles_n, tm, tn);
   for (int at = threadIdx.x; at < size / 8 * per; at += 256) {
-    const int r = blockIdx.y * (size / 8) + at / per, c = at % per * 8, m = tm * size + r, n = tn * tile_n + c;
+    const int r = blockIdx.y * (size / 8) + (at >> shift), c = (at & (per - 1)) * 8, m = tm * size + r, n = tn * tile_n + c;
     if (m >= a.m || n >= a.n) continue;
     float v[8], u[8], x[8];
 #pragma unroll
