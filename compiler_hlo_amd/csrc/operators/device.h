@@ -86,6 +86,23 @@ __device__ __forceinline__ void store8(typename T::Store *p, const float (&v)[8]
   }
 }
 
+// W consecutive elements at any alignment, in whole accesses (the hardware's
+// memory takes them unaligned).
+template <class T, int W>
+__device__ __forceinline__ void load_any(const typename T::Store *p, float (&v)[W]) {
+  typename T::Store t[W];
+  __builtin_memcpy(t, p, sizeof t);
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = T::load(t[i]);
+}
+template <class T, int W>
+__device__ __forceinline__ void store_any(typename T::Store *p, const float (&v)[W]) {
+  typename T::Store t[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) t[i] = T::store(v[i]);
+  __builtin_memcpy(p, t, sizeof t);
+}
+
 // Four consecutive elements; p is 8-byte (16-bit types) or 16-byte (f32)
 // aligned.
 template <class T>

@@ -524,7 +524,7 @@ hipError_t place(const Call &c, const Operand &o, const void *src, int64_t elem,
   if (o.pack_at < 0 || o.rows == 0) return hipSuccess;
   void *dst = c.ws + o.pack_at;
   *at = dst;
-  return launch_pack(src, o.src_ld, dst, o.ld, o.rows, o.src_cols, (int)elem, c.stream);
+  return launch_pack(src, o.src_ld * elem, dst, o.ld * elem, o.rows, o.src_cols * elem, c.stream);
 }
 
 ProductArgs args_of(const Call &c, const Product &p, const void *a, const void *b, int64_t elem, const Epilogue &e) {

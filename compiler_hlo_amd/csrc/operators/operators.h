@@ -70,9 +70,10 @@ struct ActGradArgs {
 hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s);
 int act_grad_groups(int64_t m, int64_t n);
 
-// dst (rows of ld_dst elements) = src with the tail of every row zero.
-hipError_t launch_pack(const void *src, int64_t ld_src, void *dst, int64_t ld_dst, int64_t rows, int64_t cols,
-                       int elem_bytes, hipStream_t s);
+// dst = src with the tail of every row zero.  In bytes; dst and ld_dst are
+// multiples of 16.
+hipError_t launch_pack(const void *src, int64_t ld_src, void *dst, int64_t ld_dst, int64_t rows, int64_t bytes,
+                       hipStream_t s);
 
 // ---- products (product.hip, skinny.hip) ----------------------------------
 // What happens to a row's four consecutive sums (product_epilogue.h).

@@ -16,6 +16,8 @@ __device__ __forceinline__ void get(const void *base, int64_t at, int left, bool
     const f32x4 x = load4<E>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = x[i];
+  } else if (left >= W) {
+    load_any<E, W>(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = i < left ? E::load(p[i]) : 0.f;
@@ -32,6 +34,8 @@ __device__ __forceinline__ void put(void *base, int64_t at, int left, bool vec, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = v[i];
     store4<E>(p, x);
+  } else if (left >= W) {
+    store_any<E, W>(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i)
