@@ -99,7 +99,8 @@ struct ProductArgs {
   int32_t tiles_full;        // tiles 0 and 1: so many are one workgroup's, the others `splits` workgroups'
   int32_t splits, k_tiles_per_split;
   // splits > 1: [splits][shared tiles][part_rows][part_cols], the up half's
-  // columns after the gate's, or (strips, skinny) [splits][m][ldp]
+  // columns after the gate's, or (strips, skinny) [splits][m][ldp]; s8: 32-bit
+  // integers
   float *partial;
   int32_t part_rows, part_cols;
   int64_t ldp;
@@ -122,6 +123,6 @@ struct SkinnyArgs {
 hipError_t launch_skinny(const SkinnyArgs &a, hipStream_t s);
 
 // Sum the partials of strips or of skinny products and run the epilogue.
-hipError_t launch_product_fold(const float *partial, int splits, int64_t ldp, const Epilogue &e, hipStream_t s);
+hipError_t launch_product_fold(const ProductArgs &a, hipStream_t s);
 
 }  // namespace hf

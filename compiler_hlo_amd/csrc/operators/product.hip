@@ -346,6 +346,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   // consecutive columns of a row and a row's stores are contiguous.  A lane's
   // four sums are 16 bytes; the pad keeps neighbouring rows in different banks.
   const int l = threadIdx.x % 64;
+  const bool shared = part && a.splits > 1;
   float *out = (float *)lds;
   const int shift = __builtin_ctz(tile_n / 8), per = 1 << shift;  // threads a row
 #pragma unroll
@@ -358,7 +359,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
 #pragma unroll
         for (int y = 0; y < TN; ++y)
           *(f32x4 *)(out + (wm * (HM / 2) + x * 16 + (l & 15)) * kPitch + j * HN + wn * 32 + y * 16 + (l >> 4) * 4) =
-              Step::sums(acc[i][j][x][y]);
+              shared ? Step::bits(acc[i][j][x][y]) : Step::sums(acc[i][j][x][y]);
     __syncthreads();
 #pragma unroll 1
     for (int at = threadIdx.x; at < HM * per; at += THREADS) {
@@ -366,7 +367,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
       float v[8], u[8];
       load8<F32>(out + r * kPitch + c, v);
       if (gated) load8<F32>(out + r * kPitch + HN + c, u);
-      if (part && a.splits > 1) {
+      if (shared) {
         if (i * HM + r < a.part_rows && c < (gated ? a.part_cols / 2 : a.part_cols)) {
           float *p = a.partial + (((int64_t)piece * rest + local) * a.part_rows + i * HM + r) * a.part_cols + c;
           store8<F32>(p, v);
@@ -487,7 +488,8 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
   __syncthreads();
 #pragma unroll
   for (int x = 0; x < TM; ++x)
-    *(f32x4 *)(out + (x * 16 + (l & 15)) * kPitch + half * HN + col + (l >> 4) * 4) = Step::sums(acc[x]);
+    *(f32x4 *)(out + (x * 16 + (l & 15)) * kPitch + half * HN + col + (l >> 4) * 4) =
+        a.splits > 1 ? Step::bits(acc[x]) : Step::sums(acc[x]);
   __syncthreads();
   const int shift = __builtin_ctz(width / 8), per = 1 << shift;
 #pragma unroll 1
@@ -508,6 +510,7 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
 }
 
 // The splits' partial sums, added in order, through the epilogue.
+template <bool WHOLE>
 __global__ __launch_bounds__(256) void product_fold_kernel(const float *partial, int splits, int64_t ldp, Epilogue e) {
   const int n = (blockIdx.x * 256 + threadIdx.x) * 8;
   if (n >= e.n) return;
@@ -519,18 +522,21 @@ __global__ __launch_bounds__(256) void product_fold_kernel(const float *partial,
       const float *p = partial + ((int64_t)s * e.m + m) * ldp + n;
       load8<F32>(p, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += x[i];
+      for (int i = 0; i < 8; ++i) add_part<WHOLE>(v[i], x[i]);
       if (e.gated) {
         load8<F32>(p + ldp / 2, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] += x[i];
+        for (int i = 0; i < 8; ++i) add_part<WHOLE>(u[i], x[i]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = whole_sum<WHOLE>(v[i]), u[i] = whole_sum<WHOLE>(u[i]);
     finish<8>(e, m, n, v, u);
   }
 }
 
 // The same for the shared tiles: 1/8 of a tile's rows a workgroup.
+template <bool WHOLE>
 __device__ __forceinline__ void fold_tile(const ProductArgs &a, int size, int block) {
   const bool gated = a.e.gated;
   const int tile_n = gated ? size / 2 : size, shift = __builtin_ctz(tile_n / 8), per = 1 << shift;
@@ -548,22 +554,25 @@ __device__ __forceinline__ void fold_tile(const ProductArgs &a, int size, int bl
       const float *p = a.partial + (((int64_t)s * rest + block) * a.part_rows + r) * a.part_cols + c;
       load8<F32>(p, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += x[i];
+      for (int i = 0; i < 8; ++i) add_part<WHOLE>(v[i], x[i]);
       if (gated) {
         load8<F32>(p + a.part_cols / 2, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] += x[i];
+        for (int i = 0; i < 8; ++i) add_part<WHOLE>(u[i], x[i]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = whole_sum<WHOLE>(v[i]), u[i] = whole_sum<WHOLE>(u[i]);
     finish<8>(a.e, m, n, v, u);
   }
 }
 
+template <bool WHOLE>
 __global__ __launch_bounds__(256) void product_tile_fold_kernel(ProductArgs a, ProductArgs b, int first, int size) {
   if ((int)blockIdx.x < first)
-    fold_tile(a, size, blockIdx.x);
+    fold_tile<WHOLE>(a, size, blockIdx.x);
   else
-    fold_tile(b, size, blockIdx.x - first);
+    fold_tile<WHOLE>(b, size, blockIdx.x - first);
 }
 
 // The tiles that are shared by workgroups, and the workgroups of a product.
@@ -577,7 +586,8 @@ unsigned groups_of(const ProductArgs &a) { return (unsigned)(a.tiles_full + shar
 hipError_t fold_shared(const ProductArgs &a, const ProductArgs &b, hipStream_t s) {
   const int64_t x = a.splits > 1 ? shared_tiles(a) : 0, y = b.splits > 1 ? shared_tiles(b) : 0;
   if (x + y == 0) return hipSuccess;
-  return launch(product_tile_fold_kernel, dim3((unsigned)(x + y), 8), 256, s, a, b, (int)x, a.tile == 0 ? 256 : 128);
+  return launch(a.dtype == HF_S8 ? product_tile_fold_kernel<true> : product_tile_fold_kernel<false>,
+                dim3((unsigned)(x + y), 8), 256, s, a, b, (int)x, a.tile == 0 ? 256 : 128);
 }
 
 template <class Step>
@@ -605,7 +615,7 @@ hipError_t go_strip(const ProductArgs &a, hipStream_t s) {
   const int width = a.e.gated ? 64 : 128;
   const dim3 grid((unsigned)((a.n + width - 1) / width), (unsigned)a.splits);
   const hipError_t e = launch(strip_kernel<Step>, grid, 512, s, a);
-  return e != hipSuccess || a.splits == 1 ? e : launch_product_fold(a.partial, a.splits, a.ldp, a.e, s);
+  return e != hipSuccess || a.splits == 1 ? e : launch_product_fold(a, s);
 }
 
 template <class Step>
@@ -626,9 +636,10 @@ hipError_t launch_gradient(const ProductArgs &da, const ProductArgs &db, hipStre
   return da.dtype == HF_BF16 ? go_gradient<StepBF16>(da, db, s) : go_gradient<StepF16>(da, db, s);
 }
 
-hipError_t launch_product_fold(const float *partial, int splits, int64_t ldp, const Epilogue &e, hipStream_t s) {
-  const dim3 grid((unsigned)((e.n + 2047) / 2048), (unsigned)(e.m < 65535 ? e.m : 65535));
-  return launch(product_fold_kernel, grid, 256, s, partial, splits, ldp, e);
+hipError_t launch_product_fold(const ProductArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.e.n + 2047) / 2048), (unsigned)(a.e.m < 65535 ? a.e.m : 65535));
+  return launch(a.dtype == HF_S8 ? product_fold_kernel<true> : product_fold_kernel<false>, grid, 256, s, a.partial,
+                a.splits, a.ldp, a.e);
 }
 
 }  // namespace hf

@@ -113,6 +113,7 @@ struct StepBF16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b[i]), __builtin_bit_cast(bf16x8, a[i]), c, 0, 0, 0);
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
+  static __device__ __forceinline__ f32x4 bits(Acc c) { return c; }
 };
 struct StepF16 {
   typedef f32x4 Acc;
@@ -123,6 +124,7 @@ struct StepF16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b[i]), __builtin_bit_cast(f16x8, a[i]), c, 0, 0, 0);
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
+  static __device__ __forceinline__ f32x4 bits(Acc c) { return c; }
 };
 // e4m3, for results that promise 32-bit sums: the values, exact in f16,
 // through the f16 instructions at half the f8 rate.
@@ -146,6 +148,7 @@ struct StepF8Wide {
     return c;
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
+  static __device__ __forceinline__ f32x4 bits(Acc c) { return c; }
 };
 // e4m3: 32 bytes a lane, block scales of 2^0 (0x7f in e8m0).  The accumulator
 // is f32, but the instruction adds its 128 products with an error of up to
@@ -164,8 +167,11 @@ struct StepF8 {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
+  static __device__ __forceinline__ f32x4 bits(Acc c) { return c; }
 };
-// s8: sums in 32-bit integers, exact up to contractions of 2^17
+// s8: sums in 32-bit integers, exact up to contractions of 2^17.  Parts of a
+// sum stay integers until they are added (bits, whole_sum): rounded to f32 one
+// by one, parts of 2^30 that cancel would leave an error of 64 units.
 struct StepS8 {
   typedef i32x4 Acc;
   static constexpr bool kWide = false;
@@ -180,7 +186,18 @@ struct StepS8 {
     for (int i = 0; i < 4; ++i) v[i] = (float)c[i];
     return v;
   }
+  static __device__ __forceinline__ f32x4 bits(Acc c) { return __builtin_bit_cast(f32x4, c); }
 };
+
+// Adds a part of a sum as Step::bits left it (WHOLE: s8), and the sum's value.
+template <bool WHOLE>
+__device__ __forceinline__ void add_part(float &sum, float part) {
+  sum = WHOLE ? __int_as_float(__float_as_int(sum) + __float_as_int(part)) : sum + part;
+}
+template <bool WHOLE>
+__device__ __forceinline__ float whole_sum(float sum) {
+  return WHOLE ? (float)__float_as_int(sum) : sum;
+}
 
 template <class Step>
 __device__ __forceinline__ typename Step::Acc mma(const i32x4 (&a)[2], const i32x4 (&b)[2], typename Step::Acc c) {

@@ -21,7 +21,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
   constexpr int NB = GATED ? 2 : 1;
   constexpr int Q = 2, kBlock = Q * 128;  // steps and bytes of a block
   typedef typename Step::Acc Acc;
-  __shared__ __attribute__((aligned(16))) f32x4 part[WAVES / 2][NB][64];
+  __shared__ __attribute__((aligned(16))) Acc part[WAVES / 2][NB][64];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
   const int n0 = blockIdx.x * 16;
   const int bytes = a.k * Step::kBytes;
@@ -105,22 +105,19 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
   }
   // join: the upper half of the waves hands its sums to the lower half, until
   // one is left
-  f32x4 sum[NB];
-#pragma unroll
-  for (int h = 0; h < NB; ++h) sum[h] = Step::sums(acc[h]);
 #pragma unroll
   for (int half = WAVES / 2; half; half /= 2) {
     if (w >= half && w < 2 * half) {
 #pragma unroll
-      for (int h = 0; h < NB; ++h) part[w - half][h][l] = sum[h];
+      for (int h = 0; h < NB; ++h) part[w - half][h][l] = acc[h];
     }
     __syncthreads();
     if (w < half) {
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
-        const f32x4 o = part[w][h][l];
+        const Acc o = part[w][h][l];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[h][i] += o[i];
+        for (int i = 0; i < 4; ++i) acc[h][i] += o[i];
       }
     }
     __syncthreads();
@@ -130,13 +127,14 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
   if (a.splits > 1) {
     if (m < a.m && n < a.n) {
       float *p = a.partial + ((int64_t)blockIdx.y * a.m + m) * a.ldp + n;
-      *(f32x4 *)p = sum[0];
-      if (GATED) *(f32x4 *)(p + a.ldp / 2) = sum[NB - 1];
+      *(f32x4 *)p = Step::bits(acc[0]);
+      if (GATED) *(f32x4 *)(p + a.ldp / 2) = Step::bits(acc[NB - 1]);
     }
   } else {
+    const f32x4 gate = Step::sums(acc[0]), other = Step::sums(acc[NB - 1]);
     float v[4], u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = sum[0][i], u[i] = sum[NB - 1][i];
+    for (int i = 0; i < 4; ++i) v[i] = gate[i], u[i] = other[i];
     finish<4>(a.e, m, n, v, u);
   }
 }
@@ -150,7 +148,7 @@ hipError_t go(const SkinnyArgs &a, hipStream_t s) {
   } else if constexpr (!Step::kWide) {  // never planned with kWide
     e = launch(skinny_kernel<Step, GATED, 16>, grid, 1024, s, a);
   }
-  return e != hipSuccess || a.p.splits == 1 ? e : launch_product_fold(a.p.partial, a.p.splits, a.p.ldp, a.p.e, s);
+  return e != hipSuccess || a.p.splits == 1 ? e : launch_product_fold(a.p, s);
 }
 
 template <class Step>
