@@ -48,15 +48,17 @@ __device__ __forceinline__ void finish_as(const Epilogue &e, int m, int n, float
   const int left = e.n - n;
   const bool vec = e.vec && left >= W;
   if (e.a_scale) {
+    // from the left: the two scales' product may leave f32's range where the
+    // result is in it
     const float s = e.a_scale[m];
     float c[W];
     get<F32, W>(e.b_scale, n, left, vec, c);
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] *= s * c[i];
+    for (int i = 0; i < W; ++i) v[i] = v[i] * s * c[i];
     if (e.gated) {
       get<F32, W>(e.b_scale, (int64_t)e.n + n, left, vec && e.n % 4 == 0, c);
 #pragma unroll
-      for (int i = 0; i < W; ++i) up[i] *= s * c[i];
+      for (int i = 0; i < W; ++i) up[i] = up[i] * s * c[i];
     }
   }
   if (e.bias) {

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import compiler_hlo_amd as H
+import operators_reference as R
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,25 @@ def test_s8_sums_are_exact(m, n, k):
     d, z = H.GatedFeedForward(m, half, k, "s8", out_dtype="f32", activation="relu", save=True)(
         a, b[: 2 * half], one[:m].contiguous(), one[: 2 * half].contiguous())
     assert torch.equal(z, want[:, : 2 * half].float())
+
+
+@pytest.mark.parametrize("m", [1, 40, 200])
+def test_scales_of_any_size(m):
+    """z * a_scale * b_scale from the left: neither the two scales' product's
+    overflow nor its loss of bits reaches a result that is in range."""
+    n, k = 64, 1024
+    a = torch.full((m, k), 127, dtype=torch.int8, device="cuda")
+    b = torch.full((n, k), 127, dtype=torch.int8, device="cuda")
+    b[: n // 2] = 0
+    for sa, sb in ((1e-30, 3e-15), (1e25, 1e20), (1e25, 1e-30)):
+        for make in (H.Matmul, H.GatedFeedForward):
+            gated = make is H.GatedFeedForward
+            sizes = (m, n // 2 if gated else n, k)
+            d = make(*sizes, "s8", out_dtype="f32", **({"activation": "relu", "save": True} if gated else {}))(
+                a, b, torch.full((m,), sa, device="cuda"), torch.full((n,), sb, device="cuda"))
+            z = d[1] if gated else d
+            assert (z[:, : n // 2] == 0).all()
+            s = float(torch.tensor(sa)) * float(torch.tensor(sb)) * 127.0 * 127.0 * k
+            want = torch.full((m, n // 2), s, dtype=torch.float64)
+            # three roundings: the sum is whole
+            R.close(z[:, n // 2:], want, want * 3 * 2.0 ** -24, torch.float32)
