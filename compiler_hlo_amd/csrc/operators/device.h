@@ -134,22 +134,40 @@ __device__ __forceinline__ void store4(typename T::Store *p, f32x4 v) {
 }
 
 // 1 / (1 + exp(-z)) by the hardware's exp2 and reciprocal, each within one
-// ulp: exp(-z) = 2^(-z log2 e) carries the product's rounding, |z| 2^-24
-// relative, which matters only where the sigmoid is close to exp(z), itself
-// below 2^-24 of any sum it enters by then.  z = -inf gives 0, +inf gives 1.
+// ulp.  exp(-z) = 2^(-z log2 e) carries the argument's rounding, so where the
+// sigmoid falls off as exp(z) it is off by |z| 2^-24 of itself: ten units of
+// f32 at z = -20, nothing in 16 bits.  z = -inf gives 0, +inf gives 1.
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
+// The same within a few ulps for every z, for results in f32: the argument in
+// 64 bits, its part beyond f32 as a factor 1 + lo ln 2.  Where exp2 leaves the
+// range on either side there is nothing to correct.
+__device__ __forceinline__ float sigmoid_fine(double z) {
+  const double e = z * -1.4426950408889634;
+  const float hi = (float)e;
+  float x = __builtin_amdgcn_exp2f(hi);
+  if (hi > -150.f && hi < 128.f) x = __builtin_fmaf(x, (float)(e - (double)hi) * 0.6931471805599453f, x);
+  return __builtin_amdgcn_rcpf(1.0f + x);
+}
+
 // act(z) and act'(z).  GELU is the tanh form, 0.5 z (1 + tanh u) with
 // u = sqrt(2/pi) (z + 0.044715 z^3), written as z sigmoid(2u).
+// FINE: for results in f32, with GELU's cubic argument in 64 bits too; else to
+// the precision that 16 bits show.
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
 
+template <bool FINE>
 __device__ __forceinline__ float act_value(int kind, float z) {
   if (kind == HF_ACTIVATION_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
-  if (kind == HF_ACTIVATION_SILU) return z == -__builtin_inff() ? 0.f : z * sigmoid(z);
-  if (kind == HF_ACTIVATION_GELU)
-    return z == -__builtin_inff() ? 0.f : z * sigmoid(kGelu2 * z * (1.f + 0.044715f * z * z));
+  if (kind == HF_ACTIVATION_SILU) return z == -__builtin_inff() ? 0.f : z * (FINE ? sigmoid_fine((double)z) : sigmoid(z));
+  if (kind == HF_ACTIVATION_GELU) {
+    const double w = (double)z;
+    return z == -__builtin_inff() ? 0.f
+           : FINE ? z * sigmoid_fine(1.5957691216057308 * w * (1.0 + 0.044715 * w * w))
+                  : z * sigmoid(kGelu2 * z * (1.f + 0.044715f * z * z));
+  }
   return z;
 }
 
@@ -159,7 +177,7 @@ __device__ __forceinline__ float act_value(int kind, float z) {
 __device__ __forceinline__ float act_both(int kind, float z, float *d) {
   if (kind == HF_ACTIVATION_RELU) {
     *d = z > 0.f ? 1.f : 0.f;
-    return act_value(kind, z);
+    return act_value<false>(kind, z);
   }
   if (kind == HF_ACTIVATION_SILU || kind == HF_ACTIVATION_GELU) {
     const float c = z != z ? z : __builtin_fminf(__builtin_fmaxf(z, -1e4f), 1e4f);

@@ -73,7 +73,7 @@ __device__ __forceinline__ void finish_as(const Epilogue &e, int m, int n, float
   }
   if (e.act != HF_ACTIVATION_NONE) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = act_value(e.act, v[i]);
+    for (int i = 0; i < W; ++i) v[i] = act_value<E::kBytes == 4>(e.act, v[i]);
   }
   if (e.gated) {
 #pragma unroll

@@ -1,5 +1,7 @@
 """The operators where 32 or 16 bits come to their ends: sums, scales,
 activations, epsilons and gradients of unusual size."""
+import math
+
 import pytest
 import torch
 
@@ -53,3 +55,21 @@ def test_scales_of_any_size(m):
             want = torch.full((m, n // 2), s, dtype=torch.float64)
             # three roundings: the sum is whole
             R.close(z[:, n // 2:], want, want * 3 * 2.0 ** -24, torch.float32)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_of_negative_values_in_32_bits(act):
+    """Where z sigmoid(z) falls off exponentially, an f32 result keeps its
+    relative precision: exp2 and the reciprocal (a unit each, of 2^-23), the
+    argument's rest, 1 + exp and the product (half a unit each): 4 units and
+    one to spare."""
+    z = torch.cat([torch.linspace(-70, 0, 5000), torch.linspace(0, 60, 1000)]) if act == "silu" else \
+        torch.cat([torch.linspace(-9, 0, 5000), torch.linspace(0, 9, 1000)])
+    n = z.numel()
+    one = torch.ones((n, 1), dtype=torch.bfloat16, device="cuda")
+    d = H.Matmul(1, n, 1, "bf16", out_dtype="f32", bias=True, activation=act)(
+        torch.zeros((1, 1), dtype=torch.bfloat16, device="cuda"), one, z.cuda())
+    w = z.double()
+    u = w if act == "silu" else 2 * math.sqrt(2 / math.pi) * (w + 0.044715 * w ** 3)
+    want = w / (1 + torch.exp(-u))
+    R.close(d[0], want, want.abs() * 5 * 2.0 ** -23, torch.float32)
