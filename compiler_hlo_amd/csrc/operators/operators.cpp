@@ -580,6 +580,7 @@ hipError_t run_norm(const Call &c) {
   a.cols = (int)op.d.n;
   a.dtype = op.d.dtype, a.weight_dtype = op.d.weight_dtype, a.out_dtype = op.d.out_dtype;
   a.eps = (float)op.d.epsilon;
+  a.root = (float)std::sqrt(op.d.epsilon);
   a.vec = op.vec;
   return launch_norm(a, c.stream);
 }

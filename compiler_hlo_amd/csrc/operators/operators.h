@@ -18,7 +18,7 @@ struct NormArgs {
   int64_t rows;
   int32_t cols;
   int32_t dtype, weight_dtype, out_dtype;
-  float eps;
+  float eps, root;  // epsilon and its square root, which may be in f32's range alone
   bool vec;  // every row starts on 16 bytes and cols is a multiple of 8
 };
 hipError_t launch_norm(const NormArgs &a, hipStream_t s);

@@ -289,7 +289,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a) {
         widen(keep[0]);
       }
     }
-    float root = sqrtf(a.eps);
+    float root = a.root;
     const float largest = __builtin_fmaxf(row_top<T>(top, far_top_slots), root);
     int power = 0;
     (void)frexpf(largest, &power);

@@ -73,3 +73,15 @@ def test_activations_of_negative_values_in_32_bits(act):
     u = w if act == "silu" else 2 * math.sqrt(2 / math.pi) * (w + 0.044715 * w ** 3)
     want = w / (1 + torch.exp(-u))
     R.close(d[0], want, want.abs() * 5 * 2.0 ** -23, torch.float32)
+
+
+def test_norm_epsilon_outside_32_bits():
+    """Epsilon is a double: its root counts where it is in range itself."""
+    x, w = torch.zeros((3, 40), device="cuda"), torch.ones(40, device="cuda")
+    x[1] = 1e-24
+    x[2] = 1.0
+    for eps in (1e-50, 1e44):
+        y, rstd = H.RmsNorm(3, 40, "f32", eps=eps)(x, w)
+        want = (R.f64(x).square().mean(1) + eps).rsqrt()
+        R.close(rstd, want, want * 16 * 2.0 ** -24, torch.float32)
+        R.close(y, R.f64(x) * want[:, None], (R.f64(x) * want[:, None]).abs() * 18 * 2.0 ** -24, torch.float32)
