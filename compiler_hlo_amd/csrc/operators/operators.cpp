@@ -143,6 +143,13 @@ Operand operand(hf_operator &op, int64_t rows, int64_t cols, int64_t ld, int64_t
 
 int64_t tiles_of(const Product &p, int64_t tile) { return cdiv(p.m, tile) * cdiv(p.n, p.gated ? tile / 2 : tile); }
 
+// Threads of a product's tiles.
+int64_t tile_threads(const Product &p) {
+  if (!p.on || p.skinny || p.tile > 1) return 0;
+  const int64_t shared = tiles_of(p, p.tile == 0 ? 256 : 128) - p.tiles_full;
+  return (p.tiles_full + shared * p.splits) * (p.tile == 0 ? 512 : 256);
+}
+
 // The tile (first .. last: 0 the larger, 1 the smaller), and how the last
 // tiles are shared: the shortest time by a simple
 // account, in microseconds.  A round of tiles (256 of the larger, 512 of the
@@ -474,6 +481,9 @@ void make_plan(hf_operator &op) {
     case HF_OPERATOR_MATMUL: case HF_OPERATOR_GATED: plan_product(op); break;
     default: plan_product_grad(op);
   }
+  // a gradient's two products share a launch; the last rows' strip has none of these
+  if (tile_threads(op.p1) + tile_threads(op.p2) >= (int64_t(1) << 32))
+    unsupported(who + ": more tiles than a launch holds (2^32 threads)");
   for (int i = op.n_params + op.n_results; i < HF_MAX_OPERATOR_BUFFERS; ++i)
     if (d.row_stride[i]) invalid(who + ": a row stride for a buffer it does not have");
   hf_operator_info &f = op.info;

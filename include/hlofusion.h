@@ -474,7 +474,8 @@ typedef struct hf_operator hf_operator;
 /* Validate and plan.  flags: 0, or HF_CREATE_PLAN_ONLY /
  * HF_CREATE_COMPILE_ONLY (both: no GPU is touched and the handle cannot be
  * launched).  Errors: HF_ERR_INVALID, HF_ERR_UNSUPPORTED (among them a row
- * stride of 8 MB or more in a product's operand), HF_ERR_HIP, HF_ERR_NOMEM. */
+ * stride of 8 MB or more in a product's operand, and a product of more tiles
+ * than a launch holds: never below 2^37 sums), HF_ERR_HIP, HF_ERR_NOMEM. */
 hf_status hf_operator_create(const hf_operator_desc *desc, uint32_t flags, hf_operator **out);
 
 /* Copy the plan into *info. */

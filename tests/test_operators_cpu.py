@@ -224,3 +224,23 @@ def test_tile_and_split_choices(m, n, k, dtype, want):
     p = H.Matmul(m, n, k, dtype, mode="plan").plan()
     assert (p["tile_rows"], p["tile_cols"], p["splits"]) == want
     assert (p["workspace_bytes"] > 0) == (want[2] > 1)
+
+
+@pytest.mark.parametrize("make", [
+    lambda: H.Matmul(2 ** 30, 129, 8, "f8e4m3", out_dtype="bf16", mode="plan"),
+    lambda: H.GatedFeedForward(2 ** 30, 65, 8, "f8e4m3", out_dtype="bf16", mode="plan"),
+    lambda: H.MatmulGrad(2 ** 30, 1, 600, mode="plan"),
+    lambda: H.Matmul(2 ** 26, 2 ** 26, 2 ** 21, mode="plan"),
+])
+def test_more_tiles_than_a_launch_holds(make):
+    """Refused at create, not by the runtime at launch."""
+    with pytest.raises(H.FusionError) as e:
+        make()
+    assert e.value.status == "HF_ERR_UNSUPPORTED" and "tiles" in e.value.message, e.value.message
+
+
+def test_the_largest_sizes_plan():
+    for op in (H.RmsNorm(2 ** 31 - 256, 64, mode="plan"), H.Dropout(2 ** 31 - 256, 4096, mode="plan"),
+               H.RmsNormGrad(1, 2 ** 30, mode="plan"), H.Matmul(1, 2 ** 30, 8, mode="plan"),
+               H.Matmul(2 ** 30, 64, 64, mode="plan"), H.MatmulGrad(2 ** 30, 64, 64, mode="plan")):
+        assert op.plan()["algorithmic_flops"] >= 0
