@@ -133,7 +133,8 @@ class BoundLaunch:
         self.results = results[0] if len(results) == 1 else tuple(results)
         self._p = (ctypes.c_void_p * max(1, len(params)))(*[t.data_ptr() for t in params])
         self._r = (ctypes.c_void_p * len(results))(*[t.data_ptr() for t in results])
-        self._args = (op._h.value, ctypes.addressof(self._p), len(params), ctypes.addressof(self._r), len(results),
+        # the handle as the operator's own object, which close() empties
+        self._args = (op._h, ctypes.addressof(self._p), len(params), ctypes.addressof(self._r), len(results),
                       None if workspace is None else workspace.data_ptr())
         self._index = params[0].device.index
         self._launch = _launch_addresses
@@ -235,9 +236,12 @@ class Operator:
         _check(_lib.hf_operator_launch_noalloc(self._h, p, len(param_ptrs), r, len(result_ptrs), stream))
 
     def close(self):
+        """Destroy the handle; launches of it, bound ones too, are refused from
+        then on."""
         if getattr(self, "_h", None):
-            _check(_lib.hf_operator_destroy(self._h))
-            self._h = None
+            h = ctypes.c_void_p(self._h.value)
+            self._h.value = None  # in the bound launches' arguments too
+            _check(_lib.hf_operator_destroy(h))
 
     def __del__(self):
         try:

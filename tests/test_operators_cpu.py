@@ -6,6 +6,7 @@ import itertools
 
 import numpy as np
 import pytest
+import torch
 
 import compiler_hlo_amd as H
 from compiler_hlo_amd import operators as O
@@ -244,3 +245,22 @@ def test_the_largest_sizes_plan():
                H.RmsNormGrad(1, 2 ** 30, mode="plan"), H.Matmul(1, 2 ** 30, 8, mode="plan"),
                H.Matmul(2 ** 30, 64, 64, mode="plan"), H.MatmulGrad(2 ** 30, 64, 64, mode="plan")):
         assert op.plan()["algorithmic_flops"] >= 0
+
+
+def test_a_bound_launch_after_close_is_refused():
+    """The binding's object keeps no handle that has been destroyed."""
+    op = H.Matmul(4, 8, 16, mode="plan")
+
+    class Stream:
+        cuda_stream = 0
+    tensors = [torch.zeros(b.dims, dtype=torch.bfloat16) for b in op.params + op.results]
+    launch = O.BoundLaunch(op, tensors[:2], tensors[2:], None)
+    with pytest.raises(H.FusionError) as e:
+        launch(Stream)
+    assert "plan-only" in e.value.message
+    op.close()
+    for call in (lambda: launch(Stream), lambda: op.launch_ptrs([0, 0], [0])):
+        with pytest.raises(H.FusionError) as e:
+            call()
+        assert e.value.status == "HF_ERR_INVALID" and "NULL handle" in e.value.message
+    op.close()
