@@ -143,10 +143,13 @@ template <class Step, bool GATED>
 hipError_t go(const SkinnyArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)((a.p.n + 15) / 16), (unsigned)a.p.splits);
   hipError_t e = hipErrorInvalidValue;
-  if (a.waves == 8) {
-    e = launch(skinny_kernel<Step, GATED, 8>, grid, 512, s, a);
-  } else if constexpr (!Step::kWide) {  // never planned with kWide
-    e = launch(skinny_kernel<Step, GATED, 16>, grid, 1024, s, a);
+  // kWide is always planned with 8 waves; a gated product otherwise never, as
+  // its 64 strips at most are no more than 256 groups of columns
+  if constexpr (Step::kWide || !GATED) {
+    if (a.waves == 8) e = launch(skinny_kernel<Step, GATED, 8>, grid, 512, s, a);
+  }
+  if constexpr (!Step::kWide) {
+    if (a.waves == 16) e = launch(skinny_kernel<Step, GATED, 16>, grid, 1024, s, a);
   }
   return e != hipSuccess || a.p.splits == 1 ? e : launch_product_fold(a.p, s);
 }
