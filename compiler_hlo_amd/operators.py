@@ -259,7 +259,10 @@ class RmsNorm(Operator):
 
     params: x [rows, cols], weight [cols], residual [rows, cols] (residual=True)
     results: y, scale [rows] (out_dtype "s8" or "f8e4m3": y is in units of its
-    row's scale), stream = h (residual=True), rstd [rows]"""
+    row's scale), stream = h (residual=True), rstd [rows]
+
+    With a weight of ones and an 8-bit result it quantises rows for an 8-bit
+    product: h = y * (scale / rstd)."""
 
     def __init__(self, rows, cols, dtype="bf16", *, residual=False, out_dtype=None, weight_dtype=None, eps=1e-5,
                  strides=None, mode="load"):

@@ -87,13 +87,15 @@ class TrainingStep:
 
 class Served:
     """The layer in 8 bits: weights with a scale a channel, laid out once; rows
-    quantised by the norm and, between the products, by a norm of ones."""
+    quantised by the norm and, between the products, by a norm with weights of
+    one, whose rstd the product's row scales take back."""
 
     def __init__(self, master, kind="f8e4m3"):
         self.kind, self.top = kind, {"f8e4m3": 448.0, "s8": 127.0}[kind]
         self.norm = master["norm"].to(torch.bfloat16)
         self.gate_up, self.gate_up_scale = self.quantise(master["gate_up"])
-        self.down = master["down"].to(torch.bfloat16)
+        self.down, self.down_scale = self.quantise(master["down"])
+        self.ones = torch.ones(self.down.shape[1], dtype=torch.bfloat16, device=self.down.device)
         self.ops = {}
 
     def quantise(self, w):
@@ -108,10 +110,14 @@ class Served:
         if rows not in self.ops:  # handles cost microseconds and no compile
             self.ops[rows] = (H.RmsNorm(rows, hidden, "bf16", residual=True, out_dtype=self.kind),
                               H.GatedFeedForward(rows, inner, hidden, self.kind, out_dtype="bf16"),
-                              H.Matmul(rows, hidden, inner, "bf16", residual=True))
-        norm, gated, down = self.ops[rows]
+                              H.RmsNorm(rows, inner, "bf16", out_dtype=self.kind),
+                              H.Matmul(rows, hidden, inner, self.kind, residual=True))
+        norm, gated, unit, down = self.ops[rows]
         q, scale, stream, _ = norm(x, self.norm, residual)
-        return down(gated(q, self.gate_up, scale, self.gate_up_scale), self.down, stream), stream
+        h = gated(q, self.gate_up, scale, self.gate_up_scale)
+        # q scale is h rstd, so the rows themselves are q (scale / rstd)
+        q, scale, rstd = unit(h, self.ones)
+        return down(q, self.down, scale / rstd, self.down_scale, stream), stream
 
 
 def main():

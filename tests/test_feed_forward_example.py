@@ -63,3 +63,33 @@ def test_training_lowers_the_loss_and_serving_agrees():
             # two operands quantised by at most half a step each, through a
             # product of two such sums
             assert relative(R.f64(y) - v, want) < 4 * step
+
+
+def test_both_products_are_served_in_8_bits():
+    """Rows and weights of both products in 8 bits.  Each of the four arrays is
+    off by e of its norm: in e4m3 half a step of 2^-4, spread evenly, at most
+    2^-4 / sqrt(3); in s8 a step of the row's largest value / 127 over
+    sqrt(12), where that value is up to 4 times the root mean square of a normal row and 10
+    times that of the gated product's.  Gate and up are then off by sqrt(2) e,
+    their product by 1.43 of that (silu keeps a normal value's spread), and the
+    down projection adds two more: 1.42 2^-4 in all for e4m3; for s8
+    hypot(1.43 sqrt(2) 4, 4, 10) / (127 sqrt(12))."""
+    import feed_forward as F
+    g = torch.Generator(device="cuda").manual_seed(5)
+    hidden, inner = 512, 1024
+    make = lambda shape, s: torch.randn(shape, generator=g, device="cuda") * s  # noqa: E731
+    master = {"norm": torch.ones(hidden, device="cuda"), "gate_up": make((2 * inner, hidden), hidden ** -0.5),
+              "down": make((hidden, inner), inner ** -0.5)}
+    for kind, bound in (("f8e4m3", 0.1), ("s8", 0.035)):
+        served = F.Served(master, kind)
+        for rows in (1, 9, 200):
+            x = make((rows, hidden), 1.0).to(torch.bfloat16)
+            y, _ = served(x, torch.zeros_like(x))
+            products = [op for op in served.ops[rows] if not isinstance(op, F.H.RmsNorm)]
+            assert len(products) == 2 and all(b.dtype == kind for op in products for b in op.params[:2])
+            v = R.f64(x)
+            h = v * (v.square().mean(1, keepdim=True) + 1e-5).rsqrt()
+            z = h @ R.f64(master["gate_up"]).T
+            want = (torch.nn.functional.silu(z[:, :inner]) * z[:, inner:]) @ R.f64(master["down"]).T
+            # and the sum with the stream is rounded to bf16
+            assert relative(R.f64(y) - v, want) < bound + 2.0 ** -8 * float((v + want).norm() / want.norm())
