@@ -100,7 +100,7 @@ class Served:
 
     def quantise(self, w):
         scale = w.abs().amax(1) / self.top
-        q = (w / scale[:, None]).clamp(-self.top, self.top)
+        q = (w / torch.where(scale > 0, scale, 1.0)[:, None]).clamp(-self.top, self.top)
         return (q.round().to(torch.int8) if self.kind == "s8" else q.to(torch.float8_e4m3fn)), scale
 
     def __call__(self, x, residual):

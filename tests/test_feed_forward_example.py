@@ -93,3 +93,16 @@ def test_both_products_are_served_in_8_bits():
             want = (torch.nn.functional.silu(z[:, :inner]) * z[:, inner:]) @ R.f64(master["down"]).T
             # and the sum with the stream is rounded to bf16
             assert relative(R.f64(y) - v, want) < bound + 2.0 ** -8 * float((v + want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("kind", ["f8e4m3", "s8"])
+def test_a_channel_of_zeros_is_served_as_zeros(kind):
+    import feed_forward as F
+    g = torch.Generator(device="cuda").manual_seed(6)
+    master = {"norm": torch.ones(128, device="cuda"), "gate_up": torch.randn((512, 128), generator=g, device="cuda"),
+              "down": torch.randn((128, 256), generator=g, device="cuda")}
+    master["gate_up"][3] = 0.0
+    master["down"][5] = 0.0
+    x = torch.randn((4, 128), generator=g, device="cuda").to(torch.bfloat16)
+    y, stream = F.Served(master, kind)(x, torch.zeros_like(x))
+    assert torch.isfinite(y).all() and torch.equal(y[:, 5], stream[:, 5])
