@@ -302,7 +302,9 @@ class Matmul(Operator):
 
 
 class MatmulGrad(Operator):
-    """The gradient of Matmul.  The residual's gradient is dd itself.
+    """The gradient of Matmul.  The residual's gradient is dd itself.  The
+    gradient before the activation is rounded to dtype on its way into the
+    products: a program in f16 scales its loss so that it fits f16's range.
 
     params: dd [m, n], a [m, k], b [n, k], z [m, n] (with an activation)
     results: da, db, dbias [n] f32 (bias=True)"""
@@ -329,7 +331,8 @@ class GatedFeedForward(Operator):
 
 
 class GatedFeedForwardGrad(Operator):
-    """The gradient of GatedFeedForward.
+    """The gradient of GatedFeedForward.  The gradients of gate and up are
+    rounded to dtype on their way into the products, as MatmulGrad's is.
 
     params: dd [m, n], a [m, k], b [2n, k], z [m, 2n]
     results: da [m, k], db [2n, k]"""

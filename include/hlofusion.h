@@ -372,7 +372,8 @@ hf_status hf_fusion_destroy(hf_fusion *f);
  *             bias [n] out_dtype (BIAS), residual [m, n] out_dtype (RESIDUAL)
  *     results d [m, n] out_dtype, z [m, n] out_dtype (SAVE)
  * HF_OPERATOR_MATMUL_GRAD    dz = dd * activation'(z), rounded to dtype for the
- *   products; da = dz b; db = dz^T a; dbias = column sums of dz (before that
+ *   products (in f16 with its range: an infinity from 65520 on, zero below
+ *   2^-25); da = dz b; db = dz^T a; dbias = column sums of dz (before that
  *   rounding).  The residual's gradient is dd itself.
  *     params  dd [m, n], a [m, k], b [n, k], z [m, n] (an activation)
  *     results da [m, k], db [n, k] dtype, dbias [n] f32 (BIAS)
@@ -382,7 +383,7 @@ hf_status hf_fusion_destroy(hf_fusion *f);
  *     params  a [m, k], b [2n, k] dtype, a_scale [m], b_scale [2n] f32 (8-bit dtype)
  *     results d [m, n] out_dtype, z [m, 2n] out_dtype (SAVE)
  * HF_OPERATOR_GATED_GRAD     dz = (dd * u * activation'(g), dd * activation(g)),
- *   rounded to dtype; da = dz b; db = dz^T a.
+ *   rounded to dtype as above; da = dz b; db = dz^T a.
  *     params  dd [m, n], a [m, k], b [2n, k], z [m, 2n]
  *     results da [m, k], db [2n, k] dtype
  * HF_OPERATOR_DROPOUT        y = keep * x / (1 - p) + residual.  Element i of the

@@ -85,3 +85,51 @@ def test_norm_epsilon_outside_32_bits():
         want = (R.f64(x).square().mean(1) + eps).rsqrt()
         R.close(rstd, want, want * 16 * 2.0 ** -24, torch.float32)
         R.close(y, R.f64(x) * want[:, None], (R.f64(x) * want[:, None]).abs() * 18 * 2.0 ** -24, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_gradients_at_the_ends_of_their_range(dtype):
+    """dz goes through the products in the operands' type: in f16 an infinity
+    from 65520 on, which stays in its row of da and of db, and zero below
+    2^-25.  dbias is summed before that rounding; bf16 keeps all of them."""
+    m, n, k = 70, 40, 24
+    g = gen(1)
+    t = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    a, b = (torch.randint(1, 3, s, generator=g, device="cuda").to(t) for s in ((m, k), (n, k)))
+    dd, z = torch.zeros((m, n), dtype=t, device="cuda"), torch.full((m, n), 1.5, dtype=t, device="cuda")
+    dd[3, 7], dd[5, 8] = 61440.0, 2.0 ** -20
+    z[3, 7], z[5, 8] = 2.5, -11.0
+    slope = R.act("silu", torch.tensor([2.5, -11.0], dtype=torch.float64))[1].tolist()
+    big, small = 61440.0 * slope[0], 2.0 ** -20 * slope[1]
+    assert big > 65520 and abs(small) < 2.0 ** -25
+    da, db, dbias = H.MatmulGrad(m, n, k, dtype, bias=True, activation="silu")(dd, a, b, z)
+    rows, cols = torch.arange(m, device="cuda") == 3, torch.arange(n, device="cuda") == 7
+    if dtype == "f16":
+        assert (da[rows] == math.inf).all() and (db[cols] == math.inf).all()
+        assert (da[~rows] == 0).all() and (db[~cols] == 0).all()
+    else:
+        half = 2.0 ** -8
+        want = torch.zeros((m, k), dtype=torch.float64)
+        want[3], want[5] = big * R.f64(b)[7], small * R.f64(b)[8]
+        R.close(da, want, want.abs() * (half + 2.0 ** -14), t)
+        want = torch.zeros((n, k), dtype=torch.float64)
+        want[7], want[8] = big * R.f64(a)[3], small * R.f64(a)[5]
+        R.close(db, want, want.abs() * (half + 2.0 ** -14), t)
+    want = torch.zeros(n, dtype=torch.float64)
+    want[7], want[8] = big, small
+    R.close(dbias, want, want.abs() * 2.0 ** -14, torch.float32)
+    # gated: the up half's value times the gradient
+    half_n = n // 2
+    zg = torch.ones((m, n), dtype=t, device="cuda")
+    zg[:, half_n:] = 300.0
+    dg = torch.zeros((m, half_n), dtype=t, device="cuda")
+    dg[9, 2] = 300.0
+    da, db = H.GatedFeedForwardGrad(m, half_n, k, dtype, activation="relu")(dg, a, b, zg)
+    if dtype == "f16":
+        assert (da[9] == math.inf).all() and (db[2] == math.inf).all()
+    else:
+        want = 90000.0 * R.f64(b)[2] + 300.0 * R.f64(b)[half_n + 2]
+        R.close(da[9], want, want * 2 * half, t)
+    others = torch.arange(m, device="cuda") != 9
+    assert (da[others] == 0).all()
+    assert torch.equal(db[half_n + 2], 300.0 * a[9])
