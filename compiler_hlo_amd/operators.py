@@ -125,7 +125,8 @@ class BoundLaunch:
     the operator and the tensors alive.  Calling it launches once more, on
     `stream` (a torch stream; None: the current one), and returns the same
     result tensors.  The buffers belong to the stream they were made on: a
-    program that launches on another orders the two itself."""
+    program that launches on another orders the two itself, and keeps this
+    object until the launch has run."""
 
     def __init__(self, op, params, results, workspace):
         import torch
@@ -217,8 +218,13 @@ class Operator:
     def __call__(self, *params, out=None, stream=None, workspace=None):
         """Run on torch tensors; returns the result tensor, or a tuple of them.
         Results and a workspace that are not given come from torch's allocator
-        on the launch stream."""
+        on the launch stream.  With a `stream`, the program orders it after
+        whatever fills the parameters, and may drop the tensors at once: the
+        allocator is told of their use."""
         out, workspace = self._buffers(params, out, stream, workspace)
+        if stream is not None:
+            for t in (*params, *out, *([] if workspace is None else [workspace])):
+                t.record_stream(stream)
         return BoundLaunch(self, params, out, workspace)(stream)
 
     def launch_ptrs(self, param_ptrs, result_ptrs, stream: int = 0, workspace: int = 0):

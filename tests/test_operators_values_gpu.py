@@ -133,3 +133,25 @@ def test_gradients_at_the_ends_of_their_range(dtype):
     others = torch.arange(m, device="cuda") != 9
     assert (da[others] == 0).all()
     assert torch.equal(db[half_n + 2], 300.0 * a[9])
+
+
+def test_buffers_of_a_launch_on_another_stream_are_not_reused_before_it():
+    """Tensors that the program drops right after a launch on a stream of its
+    own: torch's allocator must not give their memory to the next tensor of
+    the stream they came from while that launch is still waiting."""
+    rows, cols = 64, 4096
+    op = H.RmsNorm(rows, cols, "f32", residual=True)
+    w = torch.ones(cols, device="cuda")
+    x, r, y, h = (torch.full((rows, cols), v, device="cuda") for v in (1.0, 2.0, 0.0, 0.0))
+    rstd = torch.empty(rows, device="cuda")
+    taken = {t.data_ptr() for t in (x, r, y, h)}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+    op(x, w, r, out=[y, h, rstd], stream=side)
+    del x, r, y, h
+    later = [torch.full((rows, cols), 9.0, device="cuda") for _ in range(4)]
+    assert not taken & {t.data_ptr() for t in later}
+    torch.cuda.synchronize()
+    assert (rstd - (9.0 + 1e-5) ** -0.5).abs().max() < 1e-6
