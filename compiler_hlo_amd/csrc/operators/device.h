@@ -48,13 +48,18 @@ inline hipError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, hipStr
   return hipLaunchKernel((const void *)kernel, grid, dim3(block), pointers, 0, s);
 }
 
-// A launch's number of threads in x stays below 2^32, so workgroups past 2^31
-// threads are counted on in y.  (The last row of such a grid may pass the end.)
-inline dim3 grid_of(int64_t blocks, int64_t block) {
-  const int64_t most = (int64_t(1) << 31) / block, x = blocks < most ? blocks : most;
+// A launch's number of threads in x stays below 2^32, so workgroups of BLOCK
+// threads past 2^31 are counted on in y.  (The last row of such a grid may
+// pass the end.  The width is a constant because gridDim is a load.)
+template <int BLOCK>
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t most = (int64_t(1) << 31) / BLOCK, x = blocks < most ? blocks : most;
   return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
 }
-__device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+template <int BLOCK>
+__device__ __forceinline__ int64_t block_number(unsigned x, unsigned y) {
+  return (int64_t)y * ((int64_t(1) << 31) / BLOCK) + x;
+}
 
 // Eight consecutive elements as 32-bit floats: one 16-byte access in the
 // 16-bit types, two in f32.  p is 16-byte aligned.

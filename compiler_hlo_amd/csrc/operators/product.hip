@@ -419,7 +419,7 @@ __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
 
   const bool gated = a.e.gated;
   const int width = gated ? HN : 2 * HN;
-  const int n0 = (int)(blockIdx.z * gridDim.x + blockIdx.x) * width;
+  const int n0 = (int)block_number<512>(blockIdx.x, blockIdx.z) * width;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
   constexpr int kStep = 128 / Step::kBytes;
   const int k0 = blockIdx.y * a.k_tiles_per_split;
@@ -613,7 +613,7 @@ hipError_t go_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t
 template <class Step>
 hipError_t go_strip(const ProductArgs &a, hipStream_t s) {
   const int width = a.e.gated ? 64 : 128;
-  const dim3 strips = grid_of((a.n + width - 1) / width, 512), grid(strips.x, (unsigned)a.splits, strips.y);
+  const dim3 strips = grid_of<512>((a.n + width - 1) / width), grid(strips.x, (unsigned)a.splits, strips.y);
   const hipError_t e = launch(strip_kernel<Step>, grid, 512, s, a);
   return e != hipSuccess || a.splits == 1 ? e : launch_product_fold(a, s);
 }

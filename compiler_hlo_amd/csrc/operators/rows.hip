@@ -224,7 +224,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormArgs a) {
   __shared__ uint32_t far_top_slots[T == 64 ? 1 : T / 64];
   constexpr int ROWS = T == 64 ? 4 : 1;
   const int t = threadIdx.x % T;
-  const int64_t row = block_number() * ROWS + threadIdx.x / T;
+  const int64_t row = block_number<T * ROWS>(blockIdx.x, blockIdx.y) * ROWS + threadIdx.x / T;
   if (row >= a.rows) return;  // whole waves, and no barrier follows where ROWS > 1
   typedef typename E::Store S;
   const S *x = (const S *)a.x + row * a.ldx;
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
 // a column 33 us).
 __global__ __launch_bounds__(1024) void fold_kernel(const float *partial, int groups, int64_t cols, float *out) {
   __shared__ float part[64][17];
-  const int64_t c = block_number() * 16 + threadIdx.x % 16;
+  const int64_t c = block_number<1024>(blockIdx.x, blockIdx.y) * 16 + threadIdx.x % 16;
   const int lane = threadIdx.x / 16;
   float s = 0.f;
   if (c < cols) {
@@ -539,7 +539,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a) {
   typedef typename E::Store S;
   const uint64_t key = (uint64_t)a.state[0], offset = (uint64_t)a.state[1];
   const int64_t total = a.rows * a.cols, vectors = (total + 7) / 8;
-  const int64_t v = block_number() * 256 + threadIdx.x;
+  const int64_t v = block_number<256>(blockIdx.x, blockIdx.y) * 256 + threadIdx.x;
   if (v >= vectors) return;
   const u32x4 word = philox(offset + (uint64_t)v, key);
   // arrays without gaps come as one row
@@ -688,9 +688,9 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint8_t *src, int64_t l
 
 template <class E, int OUT, int T, int NV>
 hipError_t norm_go(const NormArgs &a, hipStream_t s) {
-  const int per = T == 64 ? 4 : 1, block = T == 64 ? 256 : T;
+  constexpr int per = T == 64 ? 4 : 1, block = T * per;
   return launch(a.vec ? norm_kernel<E, OUT, T, NV, true> : norm_kernel<E, OUT, T, NV, false>,
-                grid_of((a.rows + per - 1) / per, block), block, s, a);
+                grid_of<block>((a.rows + per - 1) / per), block, s, a);
 }
 
 template <class E, int OUT>
@@ -739,7 +739,7 @@ hipError_t norm_grad_by_length(const NormGradArgs &a, hipStream_t s) {
 template <class E>
 hipError_t dropout_go(const DropoutArgs &a, hipStream_t s) {
   const int64_t vectors = (a.rows * a.cols + 7) / 8;
-  return launch(a.vec ? dropout_kernel<E, true> : dropout_kernel<E, false>, grid_of((vectors + 255) / 256, 256), 256, s, a);
+  return launch(a.vec ? dropout_kernel<E, true> : dropout_kernel<E, false>, grid_of<256>((vectors + 255) / 256), 256, s, a);
 }
 
 template <class E>
@@ -773,7 +773,7 @@ hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_column_fold(const float *partial, int groups, int64_t cols, float *out, hipStream_t s) {
-  return launch(fold_kernel, grid_of((cols + 15) / 16, 1024), 1024, s, partial, groups, cols, out);
+  return launch(fold_kernel, grid_of<1024>((cols + 15) / 16), 1024, s, partial, groups, cols, out);
 }
 
 hipError_t launch_dropout(const DropoutArgs &a, hipStream_t s) {
