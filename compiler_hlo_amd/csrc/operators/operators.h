@@ -76,7 +76,8 @@ hipError_t launch_pack(const void *src, int64_t ld_src, void *dst, int64_t ld_ds
                        hipStream_t s);
 
 // ---- products (product.hip, skinny.hip) ----------------------------------
-// What happens to a row's four consecutive sums (product_epilogue.h).
+// What happens to the sums on their way out (product_epilogue.h): eight
+// consecutive ones of a row at a time, four in the skinny product.
 struct Epilogue {
   void *d, *z;
   const void *bias, *residual;
@@ -85,7 +86,7 @@ struct Epilogue {
   int32_t out_dtype, act;
   int32_t m, n;       // the extents of d
   bool gated;         // columns n .. 2n-1 of the product are the up half
-  bool vec;           // four elements of d, z and residual go in one access
+  bool vec;           // whole groups of d, z and residual are aligned and go in one access
 };
 
 struct ProductArgs {

@@ -157,9 +157,9 @@ __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &t
 // 128 x 128 with 4 waves, two of them.  A wave has HM/2 x 32 sums in each
 // quarter of the tile; gated, the second half of the columns is the up half
 // of the first, so a lane holds gate and up of the same element.
-// Measured: 8192 x 8192 x 8192 bf16 735 us, 1.50 PFLOP/s; 4096 x 4096 x 16384
+// Measured: 8192 x 8192 x 8192 bf16 730 us, 1.51 PFLOP/s; 4096 x 4096 x 16384
 // e4m3 187 us, 2.9 PFLOP/s; 8191 x 22528 x 4096 gated bf16 with both halves
-// kept 1091 us.  The matrix cores are busy 74 - 81% of the cycles and the
+// kept 1092 us.  The matrix cores are busy 74 - 81% of the cycles and the
 // power limit holds the clock at 1.6 - 1.9 GHz; a tile's end (sums out, the
 // next tile's first loads in) is 10 us.
 template <int HM, int HN>

@@ -6,7 +6,7 @@ namespace hf {
 namespace {
 
 // A workgroup computes 16 columns of d (gated: 16 and their up half) for all
-// m <= 16 rows.  Its WAVES waves share out the contraction in blocks and join
+// rows: the matrix instructions take 16, the plan gives it up to 8.  Its WAVES waves share out the contraction in blocks and join
 // their sums through LDS at the end, so that enough loads are in flight for
 // the memory though a layer has only a few hundred column groups.  Operands go
 // from memory straight to the registers in which the matrix instructions take
