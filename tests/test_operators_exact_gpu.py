@@ -191,3 +191,55 @@ def test_gated_grad(dtype, m, n, k, tile):
     da, db = op(dd, a, b, z)
     same(da, dz @ b.double(), dtype)
     same(db, dz.t() @ a.double(), dtype)
+
+
+@pytest.mark.parametrize("dtype, m, n, k", [
+    ("bf16", 4099, 4096, 4096), ("f16", 4160, 4096, 4096), ("s8", 4099, 4096, 16384), ("f8e4m3", 4110, 4096, 16384)])
+def test_last_rows(dtype, m, n, k):
+    """A few rows past whole tiles as a product of their own: 256 tiles in one
+    round, then a skinny product or a strip; every operand and result of theirs
+    lies at an offset, rows further apart than their length."""
+    g = gen(m + k)
+    a, b = whole(g, (m, k), dtype), whole(g, (n, k), dtype)
+    z = a.double() @ b.double().t()
+    slack = magnitude(a, b) * 2.0 ** -17 if dtype == "f8e4m3" else None
+    params = [a, b]
+    if dtype in ("s8", "f8e4m3"):
+        sa, sb = powers(g, m), powers(g, n)
+        params += [sa, sb]
+        scale = sa.double()[:, None] * sb.double()
+        z, slack = z * scale, None if slack is None else slack * scale
+    out = "bf16" if dtype == "f8e4m3" else "f32"
+    bias = whole(g, (n,), out)
+    residual = torch.zeros((m, n + 24), dtype=T[out], device="cuda")[:, 8:n + 8]
+    residual.copy_(whole(g, (m, n), out))
+    op = H.Matmul(m, n, k, dtype, out_dtype=out, bias=True, activation="relu", residual=True, save=True,
+                  strides={"residual": n + 24, "d": n + 8, "z": n + 16})
+    plan = op.plan()
+    assert (plan["tile_rows"], plan["splits"]) == (256, 1) and -(-m // 256) * -(-n // 256) > 256, plan
+    d, saved = op(*params, bias, residual)
+    same(saved, z + bias.double(), out, slack)
+    same(d, (z + bias.double()).clamp(min=0) + residual.double(), out, slack)
+
+
+@pytest.mark.parametrize("dtype, m, n, k", [("bf16", 4099, 2048, 8192), ("f8e4m3", 4110, 2048, 4096), ("s8", 2060, 4096, 4096)])
+def test_gated_last_rows(dtype, m, n, k):
+    g = gen(m + k)
+    a, b = whole(g, (m, k), dtype), whole(g, (2 * n, k), dtype)
+    z = a.double() @ b.double().t()
+    slack = magnitude(a, b) * 2.0 ** -17 if dtype == "f8e4m3" else torch.zeros_like(z)
+    params = [a, b]
+    if dtype != "bf16":
+        sa, sb = powers(g, m), powers(g, 2 * n)
+        params += [sa, sb]
+        scale = sa.double()[:, None] * sb.double()
+        z, slack = z * scale, slack * scale
+    out = "bf16" if dtype == "f8e4m3" else "f32"
+    op = H.GatedFeedForward(m, n, k, dtype, out_dtype=out, activation="relu", save=True,
+                            strides={"d": n + 8, "z": 2 * n + 8})
+    plan = op.plan()
+    assert (plan["tile_rows"], plan["splits"]) == (256, 1) and -(-m // 256) * -(-n // 128) > 256, plan
+    d, saved = op(*params)
+    same(saved, z, out, slack)
+    f, u = z[:, :n].clamp(min=0), z[:, n:]
+    same(d, f * u, out, (f * u).abs() * 2.0 ** -24 + slack[:, :n] * (u.abs() + slack[:, n:]) + f * slack[:, n:])
