@@ -155,3 +155,13 @@ def test_buffers_of_a_launch_on_another_stream_are_not_reused_before_it():
     assert not taken & {t.data_ptr() for t in later}
     torch.cuda.synchronize()
     assert (rstd - (9.0 + 1e-5) ** -0.5).abs().max() < 1e-6
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activation_limits_in_32_bits(act):
+    """f32 results at 0, far values, infinities and NaN."""
+    inf, nan = math.inf, math.nan
+    z = torch.tensor([0.0, 200.0, 1e30, 3e38, inf, -200.0, -1e30, -3e38, -inf, nan], device="cuda")
+    one = torch.ones((10, 1), dtype=torch.bfloat16, device="cuda")
+    d = H.Matmul(1, 10, 1, "bf16", out_dtype="f32", bias=True, activation=act)(one[:1] * 0, one, z)[0]
+    assert torch.equal(d[:5], z[:5]) and (d[5:9] == 0).all() and torch.isnan(d[9])
