@@ -115,7 +115,7 @@ def node_attr(nd: dict) -> list:
 EXPORTS = ["hf_fusion_create", "hf_fusion_plan", "hf_fusion_source", "hf_fusion_launch",
            "hf_fusion_launch_noalloc", "hf_fusion_destroy", "hf_last_error", "hf_abi_version",
            "hf_linear_index", "hf_operator_create", "hf_operator_plan", "hf_operator_launch",
-           "hf_operator_launch_noalloc", "hf_operator_destroy"]
+           "hf_operator_launch_noalloc", "hf_operator_destroy", "hf_operator_create_extended"]
 SCRATCH_BYTES = 16 << 20  # HF_SCRATCH_BYTES: the no-allocation launch's scratch memory per GPU
 
 
@@ -376,5 +376,6 @@ class Fusion:
             pass
 
 
-from .operators import (Dropout, GatedFeedForward, GatedFeedForwardGrad, Matmul, MatmulGrad,  # noqa: E402
+from .operators import (BlockQuantize, Dropout, ExpertCombine, ExpertCombineGrad, ExpertDispatch,  # noqa: E402
+                        ExpertSort, GatedFeedForward, GatedFeedForwardGrad, Matmul, MatmulGrad,
                         Operator, RmsNorm, RmsNormGrad)

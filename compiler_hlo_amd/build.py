@@ -43,7 +43,8 @@ def embed() -> str:
 # Device code compiled into the library itself (the no-allocation launch's
 # scratch array, the operators' kernels); compiled with hipcc for gfx950,
 # without packed FP32, one process a file.
-HIP_SOURCES = ["scratch.hip", "operators/rows.hip", "operators/product.hip", "operators/skinny.hip"]
+HIP_SOURCES = ["scratch.hip", "operators/rows.hip", "operators/experts.hip", "operators/product.hip",
+               "operators/product_experts.hip", "operators/skinny.hip"]
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

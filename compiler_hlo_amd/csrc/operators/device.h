@@ -146,6 +146,35 @@ __device__ __forceinline__ void store4(typename T::Store *p, f32x4 v) {
   }
 }
 
+// One step of a wave's reduction: the value of the lane that CTRL (a data
+// parallel primitive's control) names, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, true);
+}
+
+// Over a wave: within rows of 16 lanes by shifts of 1, 2, 4 and 8, then row 0
+// into 1 and 2 into 3, then the first half into the second; lane 63 has it
+// all.  0 is neutral to both operations.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += __uint_as_float(moved<0x111, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x112, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x114, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x118, 0xf>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x142, 0xa>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x143, 0xc>(__float_as_uint(v)));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, moved<0x111, 0xf>(v));
+  v = max(v, moved<0x112, 0xf>(v));
+  v = max(v, moved<0x114, 0xf>(v));
+  v = max(v, moved<0x118, 0xf>(v));
+  v = max(v, moved<0x142, 0xa>(v));
+  v = max(v, moved<0x143, 0xc>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // 1 / (1 + exp(-z)) by the hardware's exp2 and reciprocal, each within one
 // ulp.  exp(-z) = 2^(-z log2 e) carries the argument's rounding, so where the
 // sigmoid falls off as exp(z) it is off by |z| 2^-24 of itself: ten units of

@@ -1,0 +1,334 @@
+// experts.hip -- rows by expert: (token, choice) pairs sorted by expert, the
+// tokens' rows sent to the sorted places and summed up again, and the gradient
+// of that sum.
+#include "product_epilogue.h"
+
+namespace hf {
+namespace {
+
+// ---- sort ----------------------------------------------------------------
+// A stable counting sort.  Every wave has a contiguous run of pairs and counts
+// its experts in LDS; the counts before a wave's, over the experts, the
+// chunks and the waves, are where its first pair of an expert goes.  Then it
+// goes through its run again, 64 pairs at a time: pairs of the same expert
+// find each other by a ballot for each bit of the expert's number, and their
+// rank is the number of them in lower lanes.  No order depends on time.
+//
+// One workgroup does it all for up to 8192 pairs (192 pairs of 128 experts:
+// a launch and a few dependent steps); beyond that each chunk of pairs has a
+// workgroup, and a first launch counts by chunk.
+constexpr int kSortWaves = 16, kSortMost = 1024;  // waves; experts
+
+__device__ __forceinline__ int expert_of(const SortArgs &a, int p) {
+  const int e = a.ld_expert == a.top_k ? a.expert[p] : a.expert[(int64_t)(p / a.top_k) * a.ld_expert + p % a.top_k];
+  return (uint32_t)e < (uint32_t)a.experts ? e : -1;
+}
+
+// This wave's counts of its run, in `count` [experts].
+__device__ __forceinline__ void count_run(const SortArgs &a, int from, int to, int *count) {
+  for (int p = from + (int)(threadIdx.x % 64); p < to; p += 64) {
+    const int e = expert_of(a, p);
+    if (e >= 0) atomicAdd(count + e, 1);
+  }
+}
+
+struct Run {
+  int from, to;
+  __device__ __forceinline__ explicit Run(const SortArgs &a) {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), per = a.per_chunk / kSortWaves;
+    const int64_t at = (int64_t)blockIdx.x * a.per_chunk + (int64_t)w * per;
+    from = (int)min(at, (int64_t)a.pairs);
+    to = (int)min(at + per, (int64_t)a.pairs);
+  }
+};
+
+__global__ __launch_bounds__(kSortWaves * 64) void sort_count_kernel(SortArgs a) {
+  __shared__ int count[kSortMost];
+  for (int e = threadIdx.x; e < a.experts; e += kSortWaves * 64) count[e] = 0;
+  __syncthreads();
+  const Run r(a);
+  count_run(a, r.from, r.to, count);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kSortWaves * 64) a.counts[(int64_t)blockIdx.x * a.experts + e] = count[e];
+}
+
+__global__ __launch_bounds__(kSortWaves * 64) void sort_kernel(SortArgs a) {
+  __shared__ int next[kSortWaves * kSortMost];  // [wave][experts]: counts, then the next free place
+  __shared__ int sums[kSortWaves];
+  const int t = threadIdx.x, l = t % 64, w = __builtin_amdgcn_readfirstlane(t / 64), experts = a.experts;
+  for (int i = t; i < kSortWaves * experts; i += kSortWaves * 64) next[i] = 0;
+  __syncthreads();
+  const Run r(a);
+  count_run(a, r.from, r.to, next + w * experts);
+  __syncthreads();
+  // an expert a thread: all its pairs, and those of the chunks before this one
+  int all = 0, before = 0;
+  if (t < experts) {
+    if (a.chunks == 1) {
+#pragma unroll
+      for (int i = 0; i < kSortWaves; ++i) all += next[i * experts + t];
+    } else {
+#pragma unroll 8
+      for (int c = 0; c < a.chunks; ++c) {
+        const int n = a.counts[(int64_t)c * experts + t];
+        before += c < (int)blockIdx.x ? n : 0;
+        all += n;
+      }
+    }
+  }
+  int sum = all;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(sum, d);
+    sum += l >= d ? o : 0;
+  }
+  if (l == 63) sums[w] = sum;
+  __syncthreads();
+  int first = sum - all, total = 0;
+#pragma unroll
+  for (int i = 0; i < kSortWaves; ++i) {
+    const int n = sums[i];
+    first += i < w ? n : 0;
+    total += n;
+  }
+  if (t < experts) {
+    if (blockIdx.x == 0) a.offsets[t] = first;
+    int at = first + before;
+#pragma unroll
+    for (int i = 0; i < kSortWaves; ++i) {
+      const int n = next[i * experts + t];
+      next[i * experts + t] = at;
+      at += n;
+    }
+  }
+  if (blockIdx.x == 0 && t == 0) a.offsets[experts] = total;
+  __syncthreads();
+  volatile int *mine = next + w * experts;
+  const int bits = 32 - __builtin_clz(experts);
+  for (int from = r.from; from < r.to; from += 64) {
+    const int p = from + l;
+    const int e = p < r.to ? expert_of(a, p) : -1;
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const bool set = (e >> b) & 1;
+      const uint64_t has = __ballot(set);
+      same &= set ? has : ~has;
+    }
+    int place = -1;
+    if (e >= 0) place = mine[e] + __popcll(same & ((uint64_t(1) << l) - 1));
+    // the places are read before the group's first lane moves them on
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0 && __builtin_ctzll(same) == l) mine[e] = place + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (p < r.to) {
+      a.place[a.ld_place == a.top_k ? p : (int64_t)(p / a.top_k) * a.ld_place + p % a.top_k] = place;
+      if (place >= 0) a.order[place] = p;
+    }
+  }
+  // the rows past the last have no pair
+  const int64_t chunk = (int64_t)blockIdx.x * a.per_chunk, end = min(chunk + a.per_chunk, (int64_t)a.pairs);
+  for (int64_t i = max(chunk, (int64_t)total) + t; i < end; i += kSortWaves * 64) a.order[i] = -1;
+}
+
+// ---- dispatch --------------------------------------------------------------
+// y[place[t, j]] = x[t], in bytes: a workgroup takes 4 KB of a token's row,
+// reads them once and stores them top_k times, in unaligned accesses of 16
+// bytes if need be.  Bound by the stores.
+constexpr int kPiece = 4096;
+__global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a, int64_t scale_groups) {
+  int64_t id = block_number<256>(blockIdx.x, blockIdx.y);
+  if (id < scale_groups) {
+    // scales: 64 tokens a workgroup, so that their lines are read whole
+    const int64_t token = id * 64 + threadIdx.x % 64;
+    if (token >= a.tokens) return;
+    for (int j = 0; j < a.top_k; ++j) {
+      const int p = a.place[token * a.ld_place + j];
+      if ((uint32_t)p >= (uint32_t)a.pairs) continue;
+      for (int b = threadIdx.x / 64; b < a.blocks; b += 4)
+        a.y_scale[b * a.ldy_scale + p] = a.x_scale[b * a.ldx_scale + token];
+    }
+    return;
+  }
+  id -= scale_groups;
+  const int64_t pieces = (a.bytes + kPiece - 1) / kPiece, token = id / pieces;
+  if (token >= a.tokens) return;
+  const int64_t c = (id - token * pieces) * kPiece + threadIdx.x * 16;
+  if (c >= a.bytes) return;
+  const int left = a.bytes - c < 16 ? (int)(a.bytes - c) : 16;
+  const char *x = (const char *)a.x + token * a.ldx + c;
+  char *y = (char *)a.y + c;
+  const int32_t *place = a.place + token * a.ld_place;
+  if (left == 16) {
+    u32x4 v;
+    __builtin_memcpy(&v, x, 16);
+#pragma unroll 8
+    for (int j = 0; j < a.top_k; ++j) {
+      const int p = place[j];
+      if ((uint32_t)p < (uint32_t)a.pairs) __builtin_memcpy(y + p * a.ldy, &v, 16);
+    }
+  } else {
+    for (int j = 0; j < a.top_k; ++j) {
+      const int p = place[j];
+      if ((uint32_t)p >= (uint32_t)a.pairs) continue;
+      for (int i = 0; i < left; ++i) y[p * a.ldy + i] = x[i];
+    }
+  }
+}
+
+// ---- combine ---------------------------------------------------------------
+// d[t] = sum_j weight[t, j] y[place[t, j]] + residual[t]: a thread has eight
+// columns of a token and asks for up to eight rows before it adds the first.
+// Sums are in f32, in the order of j, rounded once.
+constexpr int kAtOnce = 8;
+
+template <class E>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+  const int pieces = (a.cols + 2047) / 2048;
+  const int64_t id = block_number<256>(blockIdx.x, blockIdx.y), token = id / pieces;
+  if (token >= a.tokens) return;
+  const int c = (int)(id - token * pieces) * 2048 + threadIdx.x * 8, left = a.cols - c;
+  if (left <= 0) return;
+  const bool vec = a.vec && left >= 8;
+  const int32_t *place = a.place + token * a.ld_place;
+  const float *weight = a.weight ? a.weight + token * a.ld_weight : nullptr;
+  float sum[8], add[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = add[i] = 0.f;
+  if (a.residual) get<E, 8>(a.residual, token * a.ldr + c, left, vec, add);
+  for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
+    float v[kAtOnce][8], w[kAtOnce];
+    int p[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      p[j] = j0 + j < a.top_k ? place[j0 + j] : -1;
+      w[j] = weight && j0 + j < a.top_k ? weight[j0 + j] : 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+      if ((uint32_t)p[j] < (uint32_t)a.pairs) get<E, 8>(a.y, p[j] * a.ldy + c, left, vec, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if ((uint32_t)p[j] >= (uint32_t)a.pairs) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[j], v[j][i], sum[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] += add[i];
+  put<E, 8>(a.d, token * a.ldd + c, left, vec, sum);
+}
+
+// dy[place[t, j]] = weight[t, j] dd[t], dweight[t, j] = <dd[t], y[place[t, j]]>:
+// T threads a token, which go through its columns once for every eight choices.
+template <class E, int T>
+__global__ __launch_bounds__(256) void combine_grad_kernel(CombineArgs a) {
+  __shared__ float part[T == 64 ? 1 : kAtOnce][4];
+  constexpr int PER = 256 / T;
+  const int64_t token = block_number<256>(blockIdx.x, blockIdx.y) * PER + threadIdx.x / T;
+  if (token >= a.tokens) return;  // whole waves, and no barrier follows where PER > 1
+  const int t = threadIdx.x % T;
+  const int32_t *place = a.place + token * a.ld_place;
+  const float *weight = a.weight + token * a.ld_weight;
+  for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
+    float w[kAtOnce], dot[kAtOnce];
+    int p[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      p[j] = j0 + j < a.top_k ? place[j0 + j] : -1;
+      w[j] = j0 + j < a.top_k ? weight[j0 + j] : 0.f;
+      dot[j] = 0.f;
+    }
+    for (int c = t * 8; c < a.cols; c += T * 8) {
+      const int left = a.cols - c;
+      const bool vec = a.vec && left >= 8;
+      float g[8], v[kAtOnce][8];
+      get<E, 8>(a.dd, token * a.ldd + c, left, vec, g);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if ((uint32_t)p[j] < (uint32_t)a.pairs) get<E, 8>(a.y, p[j] * a.ldy + c, left, vec, v[j]);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if ((uint32_t)p[j] >= (uint32_t)a.pairs) continue;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dot[j] = __builtin_fmaf(g[i], v[j][i], dot[j]);
+          o[i] = w[j] * g[i];
+        }
+        put<E, 8>(a.dy, p[j] * a.lddy + c, left, vec, o);
+      }
+    }
+    if (T != 64) __syncthreads();  // the sums of the choices before are read
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const float s = wave_sum(dot[j]);
+      if (T == 64) {
+        if (t == 0 && j0 + j < a.top_k) a.dweight[token * a.ld_dweight + j0 + j] = s;
+      } else if (threadIdx.x % 64 == 0) {
+        part[j][threadIdx.x / 64] = s;
+      }
+    }
+    if (T != 64) {
+      __syncthreads();
+      if (t < kAtOnce && j0 + t < a.top_k)
+        a.dweight[token * a.ld_dweight + j0 + t] = ((part[t][0] + part[t][1]) + part[t][2]) + part[t][3];
+    }
+  }
+}
+
+template <class E>
+hipError_t combine_go(const CombineArgs &a, hipStream_t s) {
+  return launch(combine_kernel<E>, grid_of<256>(a.tokens * ((a.cols + 2047) / 2048)), 256, s, a);
+}
+
+template <class E>
+hipError_t combine_grad_go(const CombineArgs &a, hipStream_t s) {
+  if (a.cols <= 512) return launch(combine_grad_kernel<E, 64>, grid_of<256>((a.tokens + 3) / 4), 256, s, a);
+  return launch(combine_grad_kernel<E, 256>, grid_of<256>(a.tokens), 256, s, a);
+}
+
+}  // namespace
+
+void sort_chunks(int64_t pairs, int32_t *chunks, int32_t *per_chunk) {
+  const int64_t step = kSortWaves * 64;
+  int64_t per = (pairs + step - 1) / step * step;
+  if (pairs > 8192) {
+    // up to 256 chunks of 2048 pairs or more
+    per = ((pairs + 255) / 256 + step - 1) / step * step;
+    if (per < 2 * step) per = 2 * step;
+  }
+  if (per < step) per = step;
+  *per_chunk = (int32_t)per;
+  *chunks = (int32_t)(pairs > 0 ? (pairs + per - 1) / per : 1);
+}
+
+hipError_t launch_sort(const SortArgs &a, hipStream_t s) {
+  if (a.chunks > 1) {
+    const hipError_t e = launch(sort_count_kernel, dim3((unsigned)a.chunks), kSortWaves * 64, s, a);
+    if (e != hipSuccess) return e;
+  }
+  return launch(sort_kernel, dim3((unsigned)a.chunks), kSortWaves * 64, s, a);
+}
+
+hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s) {
+  const int64_t scale_groups = a.x_scale ? (a.tokens + 63) / 64 : 0;
+  return launch(dispatch_kernel, grid_of<256>(scale_groups + a.tokens * ((a.bytes + kPiece - 1) / kPiece)), 256, s, a,
+                scale_groups);
+}
+
+hipError_t launch_combine(const CombineArgs &a, hipStream_t s) {
+  if (a.dtype == HF_BF16) return combine_go<BF16>(a, s);
+  if (a.dtype == HF_F16) return combine_go<F16>(a, s);
+  return combine_go<F32>(a, s);
+}
+
+hipError_t launch_combine_grad(const CombineArgs &a, hipStream_t s) {
+  if (a.dtype == HF_BF16) return combine_grad_go<BF16>(a, s);
+  if (a.dtype == HF_F16) return combine_grad_go<F16>(a, s);
+  return combine_grad_go<F32>(a, s);
+}
+
+}  // namespace hf

@@ -24,7 +24,7 @@ struct Buffer {
   int64_t rows = 1, cols = 0, ld = 0;  // a vector: one row
   int64_t elem() const {
     switch (dtype) {
-      case HF_F32: return 4;
+      case HF_F32: case HF_S32: return 4;
       case HF_S64: return 8;
       case HF_BF16: case HF_F16: return 2;
     }
@@ -46,6 +46,7 @@ struct Product {
   bool on = false, skinny = false;
   Operand a, b;
   bool gated = false;
+  int64_t experts = 0;                 // by expert: b has one weight an expert
   int64_t m = 0, n = 0, k = 0;
   int tile = 0, splits = 1, per_split = 1, waves = 8;
   int64_t tiles_full = 0, part_rows = 0, part_cols = 0;
@@ -60,13 +61,15 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct hf_operator {
   hf_operator_desc d{};
+  int64_t experts = 0, top_k = 0;  // of an extended descriptor
   hf_operator_info info{};
   int device = -1;
   bool plan_only = false;
   hf::Buffer buf[HF_MAX_OPERATOR_BUFFERS];
   int n_params = 0, n_results = 0;
   // buffer numbers of optional operands, -1: none
-  int i_scale = -1, i_stream = -1, i_rstd = -1, i_residual = -1, i_a_scale = -1, i_bias = -1, i_z = -1, i_dbias = -1;
+  int i_scale = -1, i_stream = -1, i_rstd = -1, i_residual = -1, i_a_scale = -1, i_bias = -1, i_z = -1, i_dbias = -1,
+      i_offsets = -1, i_weight = -1;
   int64_t ws = 0;
   bool vec = false;
   // gradients of products
@@ -82,7 +85,9 @@ namespace {
 [[noreturn]] void unsupported(const std::string &m) { fail(HF_ERR_UNSUPPORTED, m); }
 
 const char *kind_name(int k) {
-  static const char *names[] = {"rms_norm", "rms_norm_grad", "matmul", "matmul_grad", "gated", "gated_grad", "dropout"};
+  static const char *names[] = {"rms_norm",    "rms_norm_grad",   "matmul",         "matmul_grad",         "gated", "gated_grad",
+                                "dropout",     "expert_sort",     "expert_dispatch", "expert_combine",
+                                "expert_combine_grad", "block_quantize"};
   return names[k];
 }
 
@@ -109,6 +114,8 @@ struct Builder {
     return next++;
   }
 };
+
+constexpr int64_t kBlock = 128;  // of block scales
 
 bool is_half(int t) { return t == HF_BF16 || t == HF_F16; }
 bool is_eight(int t) { return t == HF_S8 || t == HF_F8E4M3; }
@@ -148,6 +155,16 @@ int64_t tile_threads(const Product &p) {
   if (!p.on || p.skinny || p.tile > 1) return 0;
   const int64_t shared = tiles_of(p, p.tile == 0 ? 256 : 128) - p.tiles_full;
   return (p.tiles_full + shared * p.splits) * (p.tile == 0 ? 512 : 256);
+}
+
+// The same of products by expert, a gradient's both.
+double expert_threads(const hf_operator &op) {
+  const Product &p = op.p1, &q = op.p2;
+  double n = 0;
+  const int64_t rows = p.tile == 0 ? 256 : p.tile == 1 ? 128 : 64, cols = p.tile == 0 ? 256 : 128;
+  if (p.on) n += (double)expert_tiles(p.m, p.experts, rows, 1) * (double)cdiv(p.n, p.gated ? cols / 2 : cols);
+  if (q.on) n += (double)q.experts * (double)cdiv(q.m, rows) * (double)cdiv(q.n, cols);
+  return n * (p.tile == 1 ? 256 : 512);
 }
 
 // The tile (first .. last: 0 the larger, 1 the smaller), and how the last
@@ -272,6 +289,16 @@ void place_partials(hf_operator &op, Product &p) {
   p.partial_at = take(op, p.splits * sums * 4);
 }
 
+// Products by expert.  How the rows are shared out is not known here, so the
+// tile goes by the rows that an expert has if all have as many.
+void choose_experts(const hf_operator &op, Product &p, bool wide) {
+  p.on = p.m > 0 && p.n > 0;
+  p.experts = op.experts;
+  const int64_t rows = p.m / std::max<int64_t>(1, std::min(op.experts, p.m));
+  p.tile = rows <= 64 ? 2 : wide || rows <= 192 ? 1 : 0;
+  p.per_split = (int)std::max<int64_t>(1, cdiv(p.k, 128 / op.buf[0].elem()));
+}
+
 void plan_norm(hf_operator &op) {
   const hf_operator_desc &d = op.d;
   Builder b{op};
@@ -329,12 +356,18 @@ void plan_product(hf_operator &op) {
   const bool gated = d.kind == HF_OPERATOR_GATED;
   const int64_t wide = gated ? 2 * d.n : d.n;
   Builder b{op};
+  const int64_t weights = op.experts ? op.experts : 1;
   b.add("a", d.dtype, 2, d.m, d.k);
-  b.add("b", d.dtype, 2, wide, d.k);
-  if (is_eight(d.dtype)) {
+  b.add("b", d.dtype, 2, weights * wide, d.k);
+  if (d.flags & HF_OPERATOR_BLOCK_SCALES) {
+    const int64_t along = cdiv(d.k, kBlock), high = cdiv(d.n, kBlock);
+    op.i_a_scale = b.add("a_scale", HF_F32, 2, along, d.m);
+    b.add("b_scale", HF_F32, 2, weights * (gated ? 2 : 1) * high, along);
+  } else if (is_eight(d.dtype)) {
     op.i_a_scale = b.add("a_scale", HF_F32, 1, 1, d.m);
-    b.add("b_scale", HF_F32, 1, 1, wide);
+    b.add("b_scale", HF_F32, 1, 1, weights * wide);
   }
+  if (op.experts) op.i_offsets = b.add("offsets", HF_S32, 1, 1, op.experts + 1);
   if (d.flags & HF_OPERATOR_BIAS) op.i_bias = b.add("bias", d.out_dtype, 1, 1, d.n);
   if (d.flags & HF_OPERATOR_RESIDUAL) op.i_residual = b.add("residual", d.out_dtype, 2, d.m, d.n);
   op.n_params = b.next;
@@ -345,6 +378,8 @@ void plan_product(hf_operator &op) {
   op.vec = !gated || op.i_z < 0 || d.n % 8 == 0;
   for (int i : {op.n_params, op.i_z, op.i_residual})
     if (i >= 0 && op.buf[i].rows > 1 && op.buf[i].ld % 8) op.vec = false;
+  // an expert's scales begin at a multiple of 4 of them
+  if (op.experts && is_eight(d.dtype) && wide % 4) op.vec = false;
   const int64_t elem = op.buf[0].elem();
   Product &p = op.p1;
   p.m = d.m;
@@ -352,8 +387,12 @@ void plan_product(hf_operator &op) {
   p.gated = gated;
   if (p.m > 0 && p.n > 0) {
     p.a = operand(op, d.m, d.k, op.buf[0].ld, elem, "a");
-    p.b = operand(op, wide, d.k, op.buf[1].ld, elem, "b");
+    p.b = operand(op, weights * wide, d.k, op.buf[1].ld, elem, "b");
     p.k = p.a.pack_at >= 0 || p.b.pack_at >= 0 ? up(d.k, 16 / elem) : d.k;
+  }
+  if (op.experts) {
+    choose_experts(op, p, d.dtype == HF_F8E4M3 && f8_wide(d.out_dtype, p.k));
+    return;
   }
   const double whole = choose(d, p, elem);
   // A few rows past a multiple of 256 cost a row of tiles; where a strip (or a
@@ -379,13 +418,15 @@ void plan_product_grad(hf_operator &op) {
   const bool gated = d.kind == HF_OPERATOR_GATED_GRAD;
   const int64_t wide = gated ? 2 * d.n : d.n;
   Builder b{op};
+  const int64_t weights = op.experts ? op.experts : 1;
   b.add("dd", d.dtype, 2, d.m, d.n);
   b.add("a", d.dtype, 2, d.m, d.k);
-  b.add("b", d.dtype, 2, wide, d.k);
+  b.add("b", d.dtype, 2, weights * wide, d.k);
   if (gated || d.activation != HF_ACTIVATION_NONE) op.i_z = b.add("z", d.dtype, 2, d.m, wide);
+  if (op.experts) op.i_offsets = b.add("offsets", HF_S32, 1, 1, op.experts + 1);
   op.n_params = b.next;
   b.add("da", d.dtype, 2, d.m, d.k);
-  b.add("db", d.dtype, 2, wide, d.k);
+  b.add("db", d.dtype, 2, weights * wide, d.k);
   if (d.flags & HF_OPERATOR_BIAS) op.i_dbias = b.add("dbias", HF_F32, 1, 1, d.n);
   op.n_results = b.next - op.n_params;
   const int64_t elem = 2;
@@ -404,7 +445,7 @@ void plan_product_grad(hf_operator &op) {
   Operand a, w;
   if (d.k > 0 && wide > 0) {
     if (d.m > 0) a = operand(op, d.m, d.k, op.buf[1].ld, elem, "a");
-    w = operand(op, wide, d.k, op.buf[2].ld, elem, "b");
+    w = operand(op, weights * wide, d.k, op.buf[2].ld, elem, "b");
   }
   // da [m, k] = dz [m, wide] b [wide, k]
   Product &p = op.p1;
@@ -425,14 +466,109 @@ void plan_product_grad(hf_operator &op) {
   // whole chunks in the last row too: dz's padding is there to be read
   q.a.cols = up(wide, 8);
   q.b = a;
+  if (op.experts) {
+    choose_experts(op, p, false);
+    q.on = q.m > 0 && q.n > 0;
+    q.experts = op.experts;
+    p.tile = q.tile = std::min(p.tile, 1);
+    return;
+  }
   choose_gradient(p, q);
   place_partials(op, p);
   place_partials(op, q);
 }
 
-void make_plan(hf_operator &op) {
+void plan_sort(hf_operator &op) {
   const hf_operator_desc &d = op.d;
-  if (d.kind < 0 || d.kind > HF_OPERATOR_DROPOUT) invalid("unknown operator kind " + std::to_string(d.kind));
+  Builder b{op};
+  b.add("expert", HF_S32, 2, d.m, op.top_k);
+  op.n_params = b.next;
+  b.add("place", HF_S32, 2, d.m, op.top_k);
+  b.add("order", HF_S32, 1, 1, d.m * op.top_k);
+  b.add("offsets", HF_S32, 1, 1, op.experts + 1);
+  op.n_results = b.next - op.n_params;
+  int32_t chunks, per;
+  sort_chunks(d.m * op.top_k, &chunks, &per);
+  if (chunks > 1) op.sums_at = take(op, (int64_t)chunks * op.experts * 4);
+}
+
+void plan_dispatch(hf_operator &op) {
+  const hf_operator_desc &d = op.d;
+  const int64_t pairs = d.m * op.top_k;
+  const bool blocks = d.flags & HF_OPERATOR_BLOCK_SCALES;
+  Builder b{op};
+  b.add("x", d.dtype, 2, d.m, d.n);
+  b.add("place", HF_S32, 2, d.m, op.top_k);
+  if (blocks) op.i_a_scale = b.add("x_scale", HF_F32, 2, cdiv(d.n, kBlock), d.m);
+  else if (is_eight(d.dtype)) op.i_a_scale = b.add("x_scale", HF_F32, 1, 1, d.m);
+  op.n_params = b.next;
+  b.add("y", d.dtype, 2, pairs, d.n);
+  if (blocks) op.i_scale = b.add("y_scale", HF_F32, 2, cdiv(d.n, kBlock), pairs);
+  else if (is_eight(d.dtype)) op.i_scale = b.add("y_scale", HF_F32, 1, 1, pairs);
+  op.n_results = b.next - op.n_params;
+}
+
+void plan_combine(hf_operator &op) {
+  const hf_operator_desc &d = op.d;
+  const int64_t pairs = d.m * op.top_k;
+  const bool grad = d.kind == HF_OPERATOR_EXPERT_COMBINE_GRAD;
+  Builder b{op};
+  if (grad) b.add("dd", d.dtype, 2, d.m, d.n);
+  b.add("y", d.dtype, 2, pairs, d.n);
+  b.add("place", HF_S32, 2, d.m, op.top_k);
+  if (grad || (d.flags & HF_OPERATOR_WEIGHTS)) op.i_weight = b.add("weight", HF_F32, 2, d.m, op.top_k);
+  if (d.flags & HF_OPERATOR_RESIDUAL) op.i_residual = b.add("residual", d.dtype, 2, d.m, d.n);
+  op.n_params = b.next;
+  if (grad) {
+    b.add("dy", d.dtype, 2, pairs, d.n);
+    b.add("dweight", HF_F32, 2, d.m, op.top_k);
+  } else {
+    b.add("d", d.dtype, 2, d.m, d.n);
+  }
+  op.n_results = b.next - op.n_params;
+  op.vec = d.n % 8 == 0;
+  for (int i : {0, grad ? 1 : -1, op.i_residual, op.n_params})
+    if (i >= 0 && !aligned16(op.buf[i])) op.vec = false;
+}
+
+void plan_quantize(hf_operator &op) {
+  const hf_operator_desc &d = op.d;
+  Builder b{op};
+  b.add("x", d.dtype, 2, d.m, d.n);
+  op.n_params = 1;
+  b.add("y", HF_F8E4M3, 2, d.m, d.n);
+  b.add("scale", HF_F32, 2, cdiv(d.n, kBlock), d.m);
+  op.n_results = 2;
+  op.vec = d.n % 8 == 0 && aligned16(op.buf[0]) && (op.buf[1].rows <= 1 || op.buf[1].ld % 8 == 0);
+}
+
+// The rules that an extended descriptor's fields add.
+void check_extended(const hf_operator &op, const std::string &who) {
+  const hf_operator_desc &d = op.d;
+  const bool product = d.kind >= HF_OPERATOR_MATMUL && d.kind <= HF_OPERATOR_GATED_GRAD;
+  const bool grad = d.kind == HF_OPERATOR_MATMUL_GRAD || d.kind == HF_OPERATOR_GATED_GRAD;
+  const bool sort = d.kind == HF_OPERATOR_EXPERT_SORT;
+  const bool pairs = d.kind >= HF_OPERATOR_EXPERT_SORT && d.kind <= HF_OPERATOR_EXPERT_COMBINE_GRAD;
+  if (op.experts < 0 || (sort && op.experts < 1) || (!sort && !product && op.experts))
+    invalid(who + ": experts of " + std::to_string(op.experts));
+  if (op.experts > HF_MAX_EXPERTS) unsupported(who + ": more than " + std::to_string(HF_MAX_EXPERTS) + " experts");
+  if (pairs ? op.top_k < 1 : op.top_k != 0) invalid(who + ": top_k of " + std::to_string(op.top_k));
+  int64_t count = 0;
+  if (pairs && (__builtin_mul_overflow(d.m, op.top_k, &count) || count > 0x7ff00000 || op.top_k > HF_MAX_EXPERTS))
+    unsupported(who + ": too many pairs of a token and an expert");
+  if (sort && (d.n || d.k)) invalid(who + ": n and k must be 0");
+  if ((d.flags & HF_OPERATOR_BLOCK_SCALES) && (grad || d.dtype != HF_F8E4M3))
+    invalid(who + ": block scales are f8e4m3's");
+  if (product && op.experts) {
+    if (d.flags & (HF_OPERATOR_RESIDUAL | HF_OPERATOR_BIAS)) unsupported(who + ": a bias or a residual by expert");
+    if (op.experts * d.n * 2 > (int64_t(1) << 31)) unsupported(who + ": weights of more than 2^31 rows");
+  }
+}
+
+void make_plan(hf_operator &op, bool extended) {
+  const hf_operator_desc &d = op.d;
+  if (d.kind < 0 || d.kind > (extended ? HF_OPERATOR_BLOCK_QUANTIZE : HF_OPERATOR_DROPOUT))
+    invalid("unknown operator kind " + std::to_string(d.kind));
   const std::string who = kind_name(d.kind);
   const bool product = d.kind >= HF_OPERATOR_MATMUL && d.kind <= HF_OPERATOR_GATED_GRAD;
   const bool grad = d.kind == HF_OPERATOR_MATMUL_GRAD || d.kind == HF_OPERATOR_GATED_GRAD;
@@ -448,13 +584,23 @@ void make_plan(hf_operator &op) {
   if (!product && d.k != 0) invalid(who + ": k must be 0");
   static const uint32_t allowed[] = {HF_OPERATOR_RESIDUAL, HF_OPERATOR_RESIDUAL,
                                      HF_OPERATOR_RESIDUAL | HF_OPERATOR_BIAS | HF_OPERATOR_SAVE, HF_OPERATOR_BIAS,
-                                     HF_OPERATOR_SAVE, 0, HF_OPERATOR_RESIDUAL};
-  if (d.flags & ~allowed[d.kind]) invalid(who + ": flags it does not take");
+                                     HF_OPERATOR_SAVE, 0, HF_OPERATOR_RESIDUAL, 0, HF_OPERATOR_BLOCK_SCALES,
+                                     HF_OPERATOR_RESIDUAL | HF_OPERATOR_WEIGHTS, 0, 0};
+  const bool forward = d.kind == HF_OPERATOR_MATMUL || d.kind == HF_OPERATOR_GATED;
+  if (d.flags & ~(allowed[d.kind] | (extended && forward ? HF_OPERATOR_BLOCK_SCALES : 0))) invalid(who + ": flags it does not take");
   if (d.dtype < HF_F32 || d.dtype > HF_S64 || d.out_dtype < HF_F32 || d.out_dtype > HF_S64)
     invalid(who + ": unknown element type");
   if (d.activation < HF_ACTIVATION_NONE || d.activation > HF_ACTIVATION_SILU || (!product && d.activation))
     invalid(who + ": unknown or misplaced activation");
-  if (product) {
+  if (extended) check_extended(op, who);
+  if (d.kind == HF_OPERATOR_EXPERT_SORT) {
+  } else if (d.kind == HF_OPERATOR_EXPERT_DISPATCH) {
+    if (!is_half(d.dtype) && !is_eight(d.dtype) && d.dtype != HF_F32) unsupported(who + ": this element type");
+    if (d.out_dtype != d.dtype) unsupported(who + ": results of this element type");
+  } else if (d.kind == HF_OPERATOR_BLOCK_QUANTIZE) {
+    if (!is_half(d.dtype) && d.dtype != HF_F32) unsupported(who + ": this element type");
+    if (d.out_dtype != HF_F8E4M3) unsupported(who + ": results of this element type");
+  } else if (product) {
     const bool ok = grad ? is_half(d.dtype) : is_half(d.dtype) || is_eight(d.dtype);
     if (!ok) unsupported(who + ": operands of this element type");
     if (grad ? d.out_dtype != d.dtype : !is_half(d.out_dtype) && d.out_dtype != HF_F32)
@@ -479,10 +625,17 @@ void make_plan(hf_operator &op) {
     case HF_OPERATOR_RMS_NORM_GRAD: plan_norm_grad(op); break;
     case HF_OPERATOR_DROPOUT: plan_dropout(op); break;
     case HF_OPERATOR_MATMUL: case HF_OPERATOR_GATED: plan_product(op); break;
+    case HF_OPERATOR_EXPERT_SORT: plan_sort(op); break;
+    case HF_OPERATOR_EXPERT_DISPATCH: plan_dispatch(op); break;
+    case HF_OPERATOR_EXPERT_COMBINE: case HF_OPERATOR_EXPERT_COMBINE_GRAD: plan_combine(op); break;
+    case HF_OPERATOR_BLOCK_QUANTIZE: plan_quantize(op); break;
     default: plan_product_grad(op);
   }
+  if (op.experts && product) {
+    if (expert_threads(op) >= 4e9) unsupported(who + ": more tiles than a launch holds (2^32 threads)");
+  }
   // a gradient's two products share a launch; the last rows' strip has none of these
-  if (tile_threads(op.p1) + tile_threads(op.p2) >= (int64_t(1) << 32))
+  else if (tile_threads(op.p1) + tile_threads(op.p2) >= (int64_t(1) << 32))
     unsupported(who + ": more tiles than a launch holds (2^32 threads)");
   for (int i = op.n_params + op.n_results; i < HF_MAX_OPERATOR_BUFFERS; ++i)
     if (d.row_stride[i]) invalid(who + ": a row stride for a buffer it does not have");
@@ -550,6 +703,19 @@ ProductArgs args_of(const Call &c, const Product &p, const void *a, const void *
   g.a_bytes = p.a.rows > 0 ? (p.a.rows - 1) * g.lda + p.a.cols * elem : 0;
   g.b_bytes = p.b.rows > 0 ? (p.b.rows - 1) * g.ldb + p.b.cols * elem : 0;
   g.b_half = p.gated ? p.n * g.ldb : 0;
+  if (p.experts) {
+    const int64_t rows = p.b.rows / p.experts;
+    g.b_bytes = rows > 0 ? (rows - 1) * g.ldb + p.b.cols * elem : 0;
+    g.b_expert = rows * g.ldb;
+    g.offsets = (const int32_t *)c.in(c.op->i_offsets);
+    g.experts = (int)p.experts;
+  }
+  if (c.op->d.flags & HF_OPERATOR_BLOCK_SCALES) {
+    const int i = c.op->i_a_scale;
+    g.a_scale = (const float *)c.in(i), g.lda_scale = c.ld(i);
+    g.b_scale = (const float *)c.in(i + 1), g.ldb_scale = c.ld(i + 1);
+    g.b_scale_half = (int)cdiv(p.n, kBlock);
+  }
   g.m = (int)p.m;
   g.n = (int)p.n;
   g.k = (int)p.k;
@@ -564,9 +730,12 @@ ProductArgs args_of(const Call &c, const Product &p, const void *a, const void *
   return g;
 }
 
-hipError_t run_product(const Call &c, const Product &p, const void *a, const void *b, int64_t elem, const Epilogue &e) {
+hipError_t run_product(const Call &c, const Product &p, const void *a, const void *b, int64_t elem, const Epilogue &e,
+                       int64_t from = 0) {
   if (!p.on) return hipSuccess;
-  const ProductArgs g = args_of(c, p, a, b, elem, e);
+  ProductArgs g = args_of(c, p, a, b, elem, e);
+  if (g.a_scale) g.a_scale += from;  // the first of these rows
+  if (p.experts) return launch_experts(g, c.stream);
   if (!p.skinny) return launch_product(g, c.stream);
   SkinnyArgs s{};
   s.p = g;
@@ -651,7 +820,7 @@ hipError_t run_product_forward(const Call &c) {
   e.z = c.out(op.i_z), e.ldz = c.ld(op.i_z);
   e.bias = c.in(op.i_bias);
   e.residual = c.in(op.i_residual), e.ldr = c.ld(op.i_residual);
-  if (op.i_a_scale >= 0) {
+  if (op.i_a_scale >= 0 && !(op.d.flags & HF_OPERATOR_BLOCK_SCALES)) {
     e.a_scale = (const float *)c.in(op.i_a_scale);
     e.b_scale = (const float *)c.in(op.i_a_scale + 1);
   }
@@ -676,7 +845,7 @@ hipError_t run_product_forward(const Call &c) {
   if (e.z) e.z = (char *)e.z + from * e.ldz * out;
   if (e.residual) e.residual = (const char *)e.residual + from * e.ldr * out;
   if (e.a_scale) e.a_scale += from;
-  return run_product(c, op.p2, a, b, elem, e);
+  return run_product(c, op.p2, a, b, elem, e, from);
 }
 
 hipError_t run_product_grad(const Call &c) {
@@ -709,8 +878,91 @@ hipError_t run_product_grad(const Call &c) {
     e.vec = op.buf[i].rows <= 1 || op.buf[i].ld % 8 == 0;
     return e;
   };
-  return launch_gradient(args_of(c, op.p1, dz, b, 2, plain(op.n_params, op.p1)),
-                         args_of(c, op.p2, dz, a, 2, plain(op.n_params + 1, op.p2)), c.stream);
+  const ProductArgs da = args_of(c, op.p1, dz, b, 2, plain(op.n_params, op.p1));
+  ProductArgs db = args_of(c, op.p2, dz, a, 2, plain(op.n_params + 1, op.p2));
+  if (!op.experts) return launch_gradient(da, db, c.stream);
+  // a row's bytes: an expert's rows are counted on the GPU
+  db.a_bytes = op.p2.a.cols * 2;
+  db.b_bytes = op.p2.b.cols * 2;
+  return launch_experts_gradient(da, db, c.stream);
+}
+
+hipError_t run_sort(const Call &c) {
+  const hf_operator &op = *c.op;
+  SortArgs a{};
+  const int r = op.n_params;
+  a.expert = (const int32_t *)c.in(0), a.ld_expert = c.ld(0);
+  a.place = (int32_t *)c.out(r), a.ld_place = c.ld(r);
+  a.order = (int32_t *)c.out(r + 1);
+  a.offsets = (int32_t *)c.out(r + 2);
+  a.pairs = (int)(op.d.m * op.top_k);
+  a.top_k = (int)op.top_k;
+  a.experts = (int)op.experts;
+  sort_chunks(a.pairs, &a.chunks, &a.per_chunk);
+  if (a.chunks > 1) a.counts = (int32_t *)(c.ws + op.sums_at);
+  return launch_sort(a, c.stream);
+}
+
+hipError_t run_dispatch(const Call &c) {
+  const hf_operator &op = *c.op;
+  if (op.d.m == 0 || op.d.n == 0) return hipSuccess;
+  DispatchArgs a{};
+  const int y = op.n_params;
+  const int64_t elem = op.buf[0].elem();
+  a.x = c.in(0), a.ldx = c.ld(0) * elem;
+  a.y = c.out(y), a.ldy = c.ld(y) * elem;
+  a.place = (const int32_t *)c.in(1), a.ld_place = c.ld(1);
+  if (op.i_a_scale >= 0) {
+    a.x_scale = (const float *)c.in(op.i_a_scale), a.ldx_scale = c.ld(op.i_a_scale);
+    a.y_scale = (float *)c.out(op.i_scale), a.ldy_scale = c.ld(op.i_scale);
+    a.blocks = (int)op.buf[op.i_a_scale].rows;
+  }
+  a.tokens = op.d.m;
+  a.bytes = op.d.n * elem;
+  a.top_k = (int)op.top_k;
+  a.pairs = (int)(op.d.m * op.top_k);
+  return launch_dispatch(a, c.stream);
+}
+
+hipError_t run_combine(const Call &c) {
+  const hf_operator &op = *c.op;
+  const bool grad = op.d.kind == HF_OPERATOR_EXPERT_COMBINE_GRAD;
+  if (op.d.m == 0) return hipSuccess;
+  CombineArgs a{};
+  const int y = grad ? 1 : 0, r = op.n_params;
+  a.y = c.in(y), a.ldy = c.ld(y);
+  a.place = (const int32_t *)c.in(y + 1), a.ld_place = c.ld(y + 1);
+  a.weight = (const float *)c.in(op.i_weight), a.ld_weight = c.ld(op.i_weight);
+  a.residual = c.in(op.i_residual), a.ldr = c.ld(op.i_residual);
+  a.tokens = op.d.m;
+  a.cols = (int)op.d.n;
+  a.top_k = (int)op.top_k;
+  a.pairs = (int)(op.d.m * op.top_k);
+  a.dtype = op.d.dtype;
+  a.vec = op.vec;
+  if (grad) {
+    a.dd = c.in(0), a.ldd = c.ld(0);
+    a.dy = c.out(r), a.lddy = c.ld(r);
+    a.dweight = (float *)c.out(r + 1), a.ld_dweight = c.ld(r + 1);
+    return launch_combine_grad(a, c.stream);
+  }
+  if (op.d.n == 0) return hipSuccess;
+  a.d = c.out(r), a.ldd = c.ld(r);
+  return launch_combine(a, c.stream);
+}
+
+hipError_t run_quantize(const Call &c) {
+  const hf_operator &op = *c.op;
+  if (op.d.m == 0 || op.d.n == 0) return hipSuccess;
+  QuantizeArgs a{};
+  a.x = c.in(0), a.ldx = c.ld(0);
+  a.y = (uint8_t *)c.out(1), a.ldy = c.ld(1);
+  a.scale = (float *)c.out(2), a.ld_scale = c.ld(2);
+  a.rows = op.d.m;
+  a.cols = (int)op.d.n;
+  a.dtype = op.d.dtype;
+  a.vec = op.vec;
+  return launch_quantize(a, c.stream);
 }
 
 // Two buffers that share no element.  Column windows of one array (equal row
@@ -784,6 +1036,10 @@ hf_status launch_operator(const hf_operator *op, const void *const *params, int3
     case HF_OPERATOR_RMS_NORM_GRAD: e = run_norm_grad(c); break;
     case HF_OPERATOR_DROPOUT: e = run_dropout(c); break;
     case HF_OPERATOR_MATMUL: case HF_OPERATOR_GATED: e = run_product_forward(c); break;
+    case HF_OPERATOR_EXPERT_SORT: e = run_sort(c); break;
+    case HF_OPERATOR_EXPERT_DISPATCH: e = run_dispatch(c); break;
+    case HF_OPERATOR_EXPERT_COMBINE: case HF_OPERATOR_EXPERT_COMBINE_GRAD: e = run_combine(c); break;
+    case HF_OPERATOR_BLOCK_QUANTIZE: e = run_quantize(c); break;
     default: e = run_product_grad(c);
   }
   return e == hipSuccess ? HF_OK : hip_error(e, kind_name(op->d.kind));
@@ -842,28 +1098,47 @@ hf_status current_device(int *device) {
 }  // namespace
 }  // namespace hf
 
-extern "C" {
+namespace hf {
+namespace {
 
-hf_status hf_operator_create(const hf_operator_desc *desc, uint32_t flags, hf_operator **out) {
-  return hf::guarded([&]() -> hf_status {
-    hf::set_error("");
-    if (!out) hf::invalid("out is NULL");
+// desc as hf_operator_create takes it, or the whole extended one
+hf_status create(const hf_operator_desc *desc, const hf_operator_extended_desc *extended, uint32_t flags, hf_operator **out) {
+  return guarded([&]() -> hf_status {
+    set_error("");
+    if (!out) invalid("out is NULL");
     *out = nullptr;
-    if (!desc) hf::invalid("desc is NULL");
+    if (!desc) invalid("desc is NULL");
     if (desc->abi_version != HF_ABI_VERSION)
-      hf::invalid("abi_version " + std::to_string(desc->abi_version) + ", expected " + std::to_string(HF_ABI_VERSION));
-    if (flags & ~(HF_CREATE_PLAN_ONLY | HF_CREATE_COMPILE_ONLY)) hf::invalid("unknown create flags");
+      invalid("abi_version " + std::to_string(desc->abi_version) + ", expected " + std::to_string(HF_ABI_VERSION));
+    if (flags & ~(HF_CREATE_PLAN_ONLY | HF_CREATE_COMPILE_ONLY)) invalid("unknown create flags");
     std::unique_ptr<hf_operator> op(new hf_operator);
     op->d = *desc;
+    if (extended) {
+      op->experts = extended->experts;
+      op->top_k = extended->top_k;
+    }
     op->plan_only = flags != 0;
-    hf::make_plan(*op);
+    make_plan(*op, extended != nullptr);
     if (!op->plan_only) {
-      const hf_status st = hf::current_device(&op->device);
+      const hf_status st = current_device(&op->device);
       if (st != HF_OK) return st;
     }
     *out = op.release();
     return HF_OK;
   });
+}
+
+}  // namespace
+}  // namespace hf
+
+extern "C" {
+
+hf_status hf_operator_create(const hf_operator_desc *desc, uint32_t flags, hf_operator **out) {
+  return hf::create(desc, nullptr, flags, out);
+}
+
+hf_status hf_operator_create_extended(const hf_operator_extended_desc *desc, uint32_t flags, hf_operator **out) {
+  return hf::create(desc ? &desc->op : nullptr, desc, flags, out);
 }
 
 hf_status hf_operator_plan(const hf_operator *op, hf_operator_info *info) {

@@ -51,6 +51,58 @@ struct DropoutArgs {
 };
 hipError_t launch_dropout(const DropoutArgs &a, hipStream_t s);
 
+// ---- rows by expert (experts.hip) ----------------------------------------
+struct SortArgs {
+  const int32_t *expert;
+  int32_t *place, *order, *offsets;
+  int32_t *counts;               // [chunks][experts], chunks > 1
+  int64_t ld_expert, ld_place;
+  int32_t pairs, top_k, experts;
+  int32_t chunks, per_chunk;     // pairs of a workgroup
+};
+hipError_t launch_sort(const SortArgs &a, hipStream_t s);
+// The workgroups of a sort and the pairs of each.
+void sort_chunks(int64_t pairs, int32_t *chunks, int32_t *per_chunk);
+
+struct DispatchArgs {
+  const void *x;
+  void *y;
+  const int32_t *place;
+  const float *x_scale;          // [blocks][tokens] or NULL
+  float *y_scale;
+  int64_t ldx, ldy;              // bytes
+  int64_t ld_place, ldx_scale, ldy_scale;
+  int64_t tokens, bytes;         // of a row
+  int32_t top_k, pairs, blocks;
+};
+hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s);
+
+struct CombineArgs {
+  const void *y, *residual, *dd;
+  void *d, *dy;
+  const int32_t *place;
+  const float *weight;           // NULL: ones
+  float *dweight;
+  int64_t ldy, ldr, ldd, lddy, ld_place, ld_weight, ld_dweight;
+  int64_t tokens;
+  int32_t cols, top_k, pairs;
+  int32_t dtype;
+  bool vec;                      // every row starts on 16 bytes and cols is a multiple of 8
+};
+hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
+hipError_t launch_combine_grad(const CombineArgs &a, hipStream_t s);  // ldd: dd's rows
+
+struct QuantizeArgs {
+  const void *x;
+  uint8_t *y;
+  float *scale;
+  int64_t ldx, ldy, ld_scale;
+  int64_t rows;
+  int32_t cols, dtype;
+  bool vec;                      // every row starts on 16 (y: 8) bytes and cols is a multiple of 8
+};
+hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t s);
+
 // out[c] = sum of partial[g][c] over g, in a fixed order.
 hipError_t launch_column_fold(const float *partial, int groups, int64_t cols, float *out, hipStream_t s);
 
@@ -105,8 +157,26 @@ struct ProductArgs {
   float *partial;
   int32_t part_rows, part_cols;
   int64_t ldp;
+  // e4m3 with block scales (else NULL): a_scale [blocks][rows], b_scale [blocks
+  // of 128 rows][blocks], in elements; b_scale_half: blocks of rows of n, from a
+  // gate block to its up block
+  const float *a_scale, *b_scale;
+  int64_t lda_scale, ldb_scale;
+  int32_t b_scale_half;
+  // by expert (else NULL): m rows of a and d, sorted; b_bytes is one weight's,
+  // b_expert bytes lie between two
+  const int32_t *offsets;
+  int32_t experts;
+  int64_t b_expert;
   Epilogue e;
 };
+// What a launch of 256 or 512 threads a workgroup takes in tiles by expert.
+int64_t expert_tiles(int64_t m, int64_t experts, int64_t size, int64_t per);
+hipError_t launch_experts(const ProductArgs &a, hipStream_t s);
+// The gradient by expert: da as above with b's rows as the contraction; db's
+// contraction runs over an expert's rows, its a_bytes and b_bytes are a row's,
+// its rows m and its results an expert's.
+hipError_t launch_experts_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t s);
 hipError_t launch_product(const ProductArgs &a, hipStream_t s);
 // da = dz b (the contraction runs over b's rows) and db = dz^T a (over both
 // operands' rows), tiles of one size; one of them may be empty (m or n 0,

@@ -108,6 +108,7 @@ __device__ __forceinline__ void finish(const Epilogue &e, int m, int n, float (&
 // holds is the same for a and b, and their order does not matter to a sum.
 struct StepBF16 {
   typedef f32x4 Acc;
+  static constexpr bool kBlock = false;
   static constexpr bool kWide = false;
   static constexpr int kBytes = 2;
   static constexpr int kSteps = 2;
@@ -119,6 +120,7 @@ struct StepBF16 {
 };
 struct StepF16 {
   typedef f32x4 Acc;
+  static constexpr bool kBlock = false;
   static constexpr bool kWide = false;
   static constexpr int kBytes = 2;
   static constexpr int kSteps = 2;
@@ -132,6 +134,7 @@ struct StepF16 {
 // through the f16 instructions at half the f8 rate.
 struct StepF8Wide {
   typedef f32x4 Acc;
+  static constexpr bool kBlock = false;
   static constexpr bool kWide = true;
   static constexpr int kBytes = 1;
   static __device__ __forceinline__ f16x8 widen(int lo, int hi) {
@@ -160,6 +163,7 @@ struct StepF8Wide {
 // results and contractions of one step take StepF8Wide.
 struct StepF8 {
   typedef f32x4 Acc;
+  static constexpr bool kBlock = false;
   static constexpr bool kWide = false;
   static constexpr int kBytes = 1;
   static constexpr int kSteps = 1;
@@ -176,6 +180,7 @@ struct StepF8 {
 // by one, parts of 2^30 that cancel would leave an error of 64 units.
 struct StepS8 {
   typedef i32x4 Acc;
+  static constexpr bool kBlock = false;
   static constexpr bool kWide = false;
   static constexpr int kBytes = 1;
   static constexpr int kSteps = 2;
@@ -189,6 +194,63 @@ struct StepS8 {
     return v;
   }
   static __device__ __forceinline__ f32x4 bits(Acc c) { return __builtin_bit_cast(f32x4, c); }
+};
+
+// A block's scale as m 2^e, m in [1, 2) (or 0, infinite, NaN; small for a
+// denormal): e goes into the matrix instruction as its own block scale (e8m0,
+// 127 + e), which leaves the product of two m's, in [1, 4), to the vector
+// unit.  The product of two whole scales might leave f32's range where the
+// sums are in it.
+struct BlockScale {
+  float m;
+  int e;
+  BlockScale() = default;
+  __device__ __forceinline__ explicit BlockScale(float s) {
+    const int p = min(max(__builtin_amdgcn_frexp_expf(s) - 1, -127), 127);
+    m = __builtin_ldexpf(s, -p);
+    e = p + 127;
+  }
+  __device__ __forceinline__ float whole() const { return __builtin_ldexpf(m, e - 127); }
+};
+// e4m3 with block scales: a step is one block of 128 of the contraction.  Its
+// sum comes out of the matrix instruction and is added with the mantissas'
+// factor: four multiply-adds a lane beside an instruction of 32 cycles.
+struct StepF8Block {
+  typedef f32x4 Acc;
+  static constexpr bool kBlock = true;
+  static constexpr bool kWide = false;
+  static constexpr int kBytes = 1;
+  static constexpr int kSteps = 1;
+  static __device__ __forceinline__ Acc add(const i32x4 (&a)[2], const i32x4 (&b)[2], BlockScale sa, BlockScale sb, Acc c) {
+    const i32x8 x = __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    const i32x8 y = __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0, 0, 0, 0}, 0, 0, 0, sb.e, 0, sa.e);
+    const float f = sa.m * sb.m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i], f, c[i]);
+    return c;
+  }
+  static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
+  static __device__ __forceinline__ f32x4 bits(Acc c) { return c; }
+};
+// The same through f16 (see StepF8Wide); scales from the left.
+struct StepF8BlockWide {
+  typedef f32x4 Acc;
+  static constexpr bool kBlock = true;
+  static constexpr bool kWide = true;
+  static constexpr int kBytes = 1;
+  static constexpr int kSteps = 2;
+  static __device__ __forceinline__ Acc add(const i32x4 (&a)[2], const i32x4 (&b)[2], BlockScale sa, BlockScale sb, Acc c) {
+    f32x4 t = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) t = StepF8Wide::step(a, b, t, k);
+    const float p = sa.whole(), q = sb.whole();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i] * p, q, c[i]);
+    return c;
+  }
+  static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
+  static __device__ __forceinline__ f32x4 bits(Acc c) { return c; }
 };
 
 // Adds a part of a sum as Step::bits left it (WHOLE: s8), and the sum's value.

@@ -1,0 +1,105 @@
+// product_experts.hip -- products by expert: the rows of a are sorted by
+// expert, and each expert multiplies its own by its own weight.
+#include "product_tile.h"
+
+namespace hf {
+namespace {
+
+// Tiles of 2 HM rows of one expert.  How many there are is in the offsets on
+// the GPU: the grid holds as many as any offsets can ask for, and a workgroup
+// without a tile ends at once.
+template <class Step, int HM, int HN>
+__global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_kernel(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<HM, HN>::lds(Step::kBlock)];
+  const int width = a.e.gated ? HN : 2 * HN;
+  ExpertTile t;
+  if (!expert_tile(a.offsets, a.experts, a.m, 2 * HM, (a.n + width - 1) / width, blockIdx.x, t)) return;
+  product_tile<Step, false, false, HM, HN, true>(part_of(a, t.expert, t.row, t.rows), t.local, lds);
+}
+
+// Strips for up to 64 rows of an expert, bound by reading the weights.  An
+// expert with more has several; those of the same columns are neighbours and
+// run at the same time on one XCD, so that its L2 has the weights for all but
+// the first.
+template <class Step>
+__global__ __launch_bounds__(512, 2) void experts_strip_kernel(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[Strip<Step>::kLds];
+  const int width = a.e.gated ? 64 : 128;
+  ExpertTile t;
+  if (!expert_tile(a.offsets, a.experts, a.m, 64, (a.n + width - 1) / width, blockIdx.x, t)) return;
+  const int units = (t.rows + 63) / 64, strip = t.local / units, from = (t.local - strip * units) * 64;
+  strip_tile<Step>(part_of(a, t.expert, t.row + from, min(64, t.rows - from)), strip, 0, blockIdx.x / 8 * 7u, lds);
+}
+
+// The gradient: da as the products above, with b's rows as the contraction,
+// and db[e] = dz^T a over the expert's rows (zeros where it has none), in one
+// launch.
+template <class Step, int HM, int HN>
+__global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_gradient_kernel(ProductArgs da, ProductArgs db, int first) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<HM, HN>::lds(false)];
+  const int tiles_n = (max(da.n, db.n) + 2 * HN - 1) / (2 * HN);  // of one that may be empty
+  if ((int)blockIdx.x < first) {
+    ExpertTile t;
+    if (!expert_tile(da.offsets, da.experts, da.m, 2 * HM, tiles_n, blockIdx.x, t)) return;
+    product_tile<Step, false, true, HM, HN, true>(part_of(da, t.expert, t.row, t.rows), t.local, lds);
+    return;
+  }
+  const int tiles = (db.m + 2 * HM - 1) / (2 * HM) * tiles_n, all = tiles * db.experts;
+  const int block = blockIdx.x - first, xcd = block % 8, q = all / 8, r = all % 8;
+  const int id = xcd * q + min(xcd, r) + block / 8;
+  const int expert = id / tiles;
+  const int row = min(max(db.offsets[expert], 0), db.k);
+  const int rows = min(max(db.offsets[expert + 1], row), db.k) - row;
+  ProductArgs p = db;
+  p.a = (const char *)db.a + row * db.lda;
+  p.b = (const char *)db.b + row * db.ldb;
+  p.a_bytes = rows > 0 ? (rows - 1) * db.lda + db.a_bytes : 0;
+  p.b_bytes = rows > 0 ? (rows - 1) * db.ldb + db.b_bytes : 0;
+  p.k = rows;
+  p.e.d = (char *)db.e.d + expert * (int64_t)db.m * db.e.ldd * 2;
+  product_tile<Step, true, true, HM, HN, true>(p, id - expert * tiles, lds);
+}
+
+template <class Step>
+hipError_t go(const ProductArgs &a, hipStream_t s) {
+  const auto groups = [&](int64_t rows, int64_t cols) {
+    const int64_t width = a.e.gated ? cols / 2 : cols;
+    return dim3((unsigned)expert_tiles(a.m, a.experts, rows, (a.n + width - 1) / width));
+  };
+  if (a.tile == 2) return launch(experts_strip_kernel<Step>, groups(64, 128), 512, s, a);
+  if (a.tile == 1) return launch(experts_kernel<Step, 64, 64>, groups(128, 128), 256, s, a);
+  if constexpr (!Step::kWide) return launch(experts_kernel<Step, 128, 128>, groups(256, 256), 512, s, a);
+  return hipErrorInvalidValue;  // never planned with kWide
+}
+
+template <class Step>
+hipError_t go_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t s) {
+  const int64_t size = da.tile == 0 ? 256 : 128, across = ((da.n > db.n ? da.n : db.n) + size - 1) / size;
+  // a multiple of 8, so that db's tiles begin at the first XCD too
+  const int64_t first = (expert_tiles(da.m, da.experts, size, across) + 7) / 8 * 8;
+  const dim3 grid((unsigned)(first + db.experts * ((db.m + size - 1) / size) * across));
+  if (grid.x == 0) return hipSuccess;
+  return da.tile == 0 ? launch(experts_gradient_kernel<Step, 128, 128>, grid, 512, s, da, db, (int)first)
+                      : launch(experts_gradient_kernel<Step, 64, 64>, grid, 256, s, da, db, (int)first);
+}
+
+}  // namespace
+
+int64_t expert_tiles(int64_t m, int64_t experts, int64_t size, int64_t per) {
+  return (m + (m < experts ? m : experts) * (size - 1)) / size * per;
+}
+
+hipError_t launch_experts(const ProductArgs &a, hipStream_t s) {
+  const bool wide = a.dtype == HF_F8E4M3 && f8_wide(a.e.out_dtype, a.k);
+  if (a.a_scale) return wide ? go<StepF8BlockWide>(a, s) : go<StepF8Block>(a, s);
+  if (a.dtype == HF_BF16) return go<StepBF16>(a, s);
+  if (a.dtype == HF_F16) return go<StepF16>(a, s);
+  if (a.dtype == HF_F8E4M3) return wide ? go<StepF8Wide>(a, s) : go<StepF8>(a, s);
+  return go<StepS8>(a, s);
+}
+
+hipError_t launch_experts_gradient(const ProductArgs &da, const ProductArgs &db, hipStream_t s) {
+  return da.dtype == HF_BF16 ? go_gradient<StepBF16>(da, db, s) : go_gradient<StepF16>(da, db, s);
+}
+
+}  // namespace hf

@@ -1,7 +1,7 @@
 // rows.hip -- the operators that are bound by memory: the root-mean-square
 // norm and its gradient, dropout, the activation's gradient, and the copies
 // that lay out an operand.
-#include "device.h"
+#include "product_epilogue.h"
 
 namespace hf {
 namespace {
@@ -86,35 +86,6 @@ __device__ __forceinline__ void load_weight(const void *w, bool wide, int t, int
     load_row<F32, T, VEC>((const float *)w, t, j, cols, v);
   else
     load_row<E, T, VEC>((const typename E::Store *)w, t, j, cols, v);
-}
-
-// One step of a wave's reduction: the value of the lane that CTRL (a data
-// parallel primitive's control) names, 0 where there is none.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t moved(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, true);
-}
-
-// Over a wave: within rows of 16 lanes by shifts of 1, 2, 4 and 8, then row 0
-// into 1 and 2 into 3, then the first half into the second; lane 63 has it
-// all.  0 is neutral to both operations.
-__device__ __forceinline__ float wave_sum(float v) {
-  v += __uint_as_float(moved<0x111, 0xf>(__float_as_uint(v)));
-  v += __uint_as_float(moved<0x112, 0xf>(__float_as_uint(v)));
-  v += __uint_as_float(moved<0x114, 0xf>(__float_as_uint(v)));
-  v += __uint_as_float(moved<0x118, 0xf>(__float_as_uint(v)));
-  v += __uint_as_float(moved<0x142, 0xa>(__float_as_uint(v)));
-  v += __uint_as_float(moved<0x143, 0xc>(__float_as_uint(v)));
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, moved<0x111, 0xf>(v));
-  v = max(v, moved<0x112, 0xf>(v));
-  v = max(v, moved<0x114, 0xf>(v));
-  v = max(v, moved<0x118, 0xf>(v));
-  v = max(v, moved<0x142, 0xa>(v));
-  v = max(v, moved<0x143, 0xc>(v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // Over the T threads of a row.  `slots`: T/64 floats of this call's own (no
@@ -691,6 +662,78 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint8_t *src, int64_t l
   }
 }
 
+// The largest of a row of 16 lanes, in all of them.
+__device__ __forceinline__ uint32_t sixteen_max(uint32_t v) {
+  v = max(v, moved<0x121, 0xf>(v));
+  v = max(v, moved<0x122, 0xf>(v));
+  v = max(v, moved<0x124, 0xf>(v));
+  return max(v, moved<0x128, 0xf>(v));
+}
+
+// BlockQuantize: e4m3 with a scale for each block of 128 of a row, scale =
+// max|x| / 448, y = round(x / scale).  16 lanes have a block, eight elements
+// each, so its largest magnitude takes four rotations within them; a workgroup
+// takes 16 blocks of R rows, and its scales go out through LDS, the rows of a
+// block side by side.  Bound by memory.
+template <class E, int R>
+__global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
+  __shared__ float scales[R][17];
+  const int wide = (a.cols + 2047) / 2048;
+  const int64_t id = block_number<256>(blockIdx.x, blockIdx.y), group = id / wide, row0 = group * R;
+  if (row0 >= a.rows) return;
+  const int c0 = (int)(id - group * wide) * 2048, c = c0 + threadIdx.x * 8, left = a.cols - c;
+  const bool vec = a.vec && left >= 8;
+  const int rows = a.rows - row0 < R ? (int)(a.rows - row0) : R;
+  constexpr int kAhead = 4;
+#pragma unroll
+  for (int r0 = 0; r0 < R; r0 += kAhead) {
+    if (r0 >= rows) break;
+    float v[kAhead][8];
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[r][i] = 0.f;
+      if (r0 + r < rows && left > 0) get<E, 8>(a.x, (row0 + r0 + r) * a.ldx + c, left, vec, v[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[r][i]) & 0x7fffffffu);
+      const float scale = __uint_as_float(sixteen_max(top)) / 448.f;
+      if (threadIdx.x % 16 == 0) scales[r0 + r][threadIdx.x / 16] = scale;
+      const Quotient q(scale);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = q(v[r][i]);
+      const u32x2 p = pack8<HF_F8E4M3>(o);
+      if (r0 + r >= rows || left <= 0) continue;
+      uint8_t *y = a.y + (row0 + r0 + r) * a.ldy + c;
+      if (vec) {
+        __builtin_nontemporal_store(p, (u32x2 *)y);
+      } else if (left >= 8) {
+        __builtin_memcpy(y, &p, 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < left) y[i] = (uint8_t)(p[i / 4] >> (8 * (i % 4)));
+      }
+    }
+  }
+  __syncthreads();
+  const int b = threadIdx.x / R, r = threadIdx.x % R;
+  if (b < 16 && r < rows && c0 / 128 + b < (a.cols + 127) / 128) a.scale[(c0 / 128 + b) * a.ld_scale + row0 + r] = scales[r][b];
+}
+
+// 16 rows a workgroup where that still makes four workgroups a compute unit,
+// so that a block's scales go out as 64 bytes; else 4.
+template <class E>
+hipError_t quantize_go(const QuantizeArgs &a, hipStream_t s) {
+  const int64_t wide = (a.cols + 2047) / 2048;
+  if (wide * (a.rows / 16) >= 1024) return launch(quantize_kernel<E, 16>, grid_of<256>(wide * ((a.rows + 15) / 16)), 256, s, a);
+  return launch(quantize_kernel<E, 4>, grid_of<256>(wide * ((a.rows + 3) / 4)), 256, s, a);
+}
+
 template <class E, int OUT, int T, int NV>
 hipError_t norm_go(const NormArgs &a, hipStream_t s) {
   constexpr int per = T == 64 ? 4 : 1, block = T * per;
@@ -775,6 +818,12 @@ hipError_t launch_norm_grad(const NormGradArgs &a, hipStream_t s) {
                        : a.dtype == HF_F16 ? norm_grad_by_length<F16>(a, s)
                                            : norm_grad_by_length<F32>(a, s);
   return e != hipSuccess ? e : launch_column_fold(a.partial, a.groups, a.cols, a.dweight, s);
+}
+
+hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t s) {
+  if (a.dtype == HF_BF16) return quantize_go<BF16>(a, s);
+  if (a.dtype == HF_F16) return quantize_go<F16>(a, s);
+  return quantize_go<F32>(a, s);
 }
 
 hipError_t launch_column_fold(const float *partial, int groups, int64_t cols, float *out, hipStream_t s) {

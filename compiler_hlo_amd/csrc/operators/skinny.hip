@@ -36,8 +36,18 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
   Acc acc[NB];
 #pragma unroll
   for (int h = 0; h < NB; ++h) acc[h] = Acc{0, 0, 0, 0};
+  // block scales: this lane's row's and the weight's, a block a step
+  constexpr bool BLOCK = Step::kBlock;
+  const float *psa = nullptr, *psb = nullptr;
+  if (BLOCK) {
+    psa = a.a_scale + min(l & 15, a.m - 1);
+    psb = a.b_scale + (int64_t)(n0 / 128) * a.ldb_scale;
+  }
+  auto scale_a = [&](int k) { return psa[(int64_t)(k / 128) * a.lda_scale]; };
+  auto scale_b = [&](int h, int k) { return psb[h * (int64_t)a.b_scale_half * a.ldb_scale + k / 128]; };
   struct Block {
     i32x4 b[NB][Q][2], a[Q][2];
+    float sb[BLOCK ? NB : 1][BLOCK ? Q : 1], sa[BLOCK ? Q : 1];
   };
   auto load = [&](int k, Block &f) {
 #pragma unroll
@@ -47,12 +57,25 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
     }
 #pragma unroll
     for (int q = 0; q < 2 * Q; ++q) f.a[q / 2][q % 2] = *(const i32x4 *)(pa + k + q * 64);
+    if constexpr (BLOCK) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        f.sa[q] = scale_a(k + q * 128);
+#pragma unroll
+        for (int h = 0; h < NB; ++h) f.sb[h][q] = scale_b(h, k + q * 128);
+      }
+    }
   };
   auto add = [&](const Block &f) {
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
-      for (int h = 0; h < NB; ++h) acc[h] = mma<Step>(f.a[q], f.b[h][q], acc[h]);
+      for (int h = 0; h < NB; ++h) {
+        if constexpr (BLOCK)
+          acc[h] = Step::add(f.a[q], f.b[h][q], BlockScale(f.sa[q]), BlockScale(f.sb[h][q]), acc[h]);
+        else
+          acc[h] = mma<Step>(f.a[q], f.b[h][q], acc[h]);
+      }
   };
   // A workgroup's blocks begin at a place of its own and go round: with all
   // of them at the same place of rows that are a power of two apart, only
@@ -100,7 +123,12 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
         fa[q] = in ? *(const i32x4 *)(pa + c + q * 64) : i32x4{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int h = 0; h < NB; ++h) acc[h] = mma<Step>(fa, fb[h], acc[h]);
+      for (int h = 0; h < NB; ++h) {
+        if constexpr (BLOCK)
+          acc[h] = Step::add(fa, fb[h], BlockScale(scale_a(c)), BlockScale(scale_b(h, c)), acc[h]);
+        else
+          acc[h] = mma<Step>(fa, fb[h], acc[h]);
+      }
     }
   }
   // join: the upper half of the waves hands its sums to the lower half, until
@@ -164,6 +192,8 @@ hipError_t either(const SkinnyArgs &a, hipStream_t s) {
 hipError_t launch_skinny(const SkinnyArgs &a, hipStream_t s) {
   if (a.p.dtype == HF_BF16) return either<StepBF16>(a, s);
   if (a.p.dtype == HF_F16) return either<StepF16>(a, s);
+  if (a.p.a_scale)
+    return f8_wide(a.p.e.out_dtype, a.p.k) ? either<StepF8BlockWide>(a, s) : either<StepF8Block>(a, s);
   if (a.p.dtype == HF_F8E4M3)
     return f8_wide(a.p.e.out_dtype, a.p.k) ? either<StepF8Wide>(a, s) : either<StepF8>(a, s);
   return either<StepS8>(a, s);

@@ -1,6 +1,9 @@
 """The operators of a transformer's feed-forward layer (hf_operator_* in
 include/hlofusion.h): RmsNorm, Matmul, GatedFeedForward and Dropout, and the
-gradients RmsNormGrad, MatmulGrad and GatedFeedForwardGrad.
+gradients RmsNormGrad, MatmulGrad and GatedFeedForwardGrad.  For a layer of
+experts: ExpertSort, ExpertDispatch, ExpertCombine and its gradient, and the
+products with ``experts=``; for 8-bit products with block scales: BlockQuantize
+and the products with ``scales="blocks"``.
 
 Like a Fusion, an operator is an immutable handle for fixed sizes and types,
 and this module marshals arguments only.  Creating one compiles nothing and
@@ -14,6 +17,13 @@ meets::
 
     up = H.GatedFeedForward(rows, 11264, 4096, "f8e4m3", out_dtype="bf16")
     h = up(q, w, scale, w_scale)
+
+    sort = H.ExpertSort(tokens, 8, 64)
+    place, order, offsets = sort(chosen)                       # [tokens, 8] int32
+    rows = H.ExpertDispatch(tokens, 8, 4096)(x, place)
+    h = H.GatedFeedForward(tokens * 8, 1408, 4096, experts=64)(rows, w, offsets)
+    rows = H.Matmul(tokens * 8, 4096, 1408, experts=64)(h, down, offsets)
+    y = H.ExpertCombine(tokens, 8, 4096)(rows, place, weight)
 
 Tensors are [rows, columns] with adjacent elements in a row.  ``strides=``
 names buffers whose rows are further apart than their length, in elements:
@@ -35,8 +45,12 @@ OPERATOR_DTYPES = dict(DTYPES, f8e4m3=8, s64=9)
 _DTYPE_NAMES = {v: k for k, v in OPERATOR_DTYPES.items()}
 KINDS = {"rms_norm": 0, "rms_norm_grad": 1, "matmul": 2, "matmul_grad": 3, "gated": 4, "gated_grad": 5,
          "dropout": 6}
+# of an extended descriptor
+EXTENDED_KINDS = {"expert_sort": 7, "expert_dispatch": 8, "expert_combine": 9, "expert_combine_grad": 10,
+                  "block_quantize": 11}
+MAX_EXPERTS = 1024  # HF_MAX_EXPERTS
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "silu": 3}
-RESIDUAL, BIAS, SAVE = 1, 2, 4
+RESIDUAL, BIAS, SAVE, WEIGHTS, BLOCK_SCALES = 1, 2, 4, 8, 16
 
 
 class HfOperatorDesc(ctypes.Structure):
@@ -45,6 +59,10 @@ class HfOperatorDesc(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
                 ("activation", ctypes.c_int32), ("flags", ctypes.c_uint32), ("epsilon", ctypes.c_double),
                 ("probability", ctypes.c_double), ("row_stride", ctypes.c_int64 * MAX_BUFFERS)]
+
+
+class HfOperatorExtendedDesc(ctypes.Structure):
+    _fields_ = [("op", HfOperatorDesc), ("experts", ctypes.c_int64), ("top_k", ctypes.c_int64)]
 
 
 class HfBufferInfo(ctypes.Structure):
@@ -61,6 +79,9 @@ class HfOperatorInfo(ctypes.Structure):
 
 _lib.hf_operator_create.restype = ctypes.c_int
 _lib.hf_operator_create.argtypes = [ctypes.POINTER(HfOperatorDesc), ctypes.c_uint32, ctypes.POINTER(ctypes.c_void_p)]
+_lib.hf_operator_create_extended.restype = ctypes.c_int
+_lib.hf_operator_create_extended.argtypes = [ctypes.POINTER(HfOperatorExtendedDesc), ctypes.c_uint32,
+                                             ctypes.POINTER(ctypes.c_void_p)]
 _lib.hf_operator_plan.restype = ctypes.c_int
 _lib.hf_operator_plan.argtypes = [ctypes.c_void_p, ctypes.POINTER(HfOperatorInfo)]
 _lib.hf_operator_launch.restype = ctypes.c_int
@@ -154,14 +175,17 @@ class Operator:
     "plan" (validate and plan only; no GPU)."""
 
     def __init__(self, kind, params, results, m, n, k, dtype, out_dtype, *, weight_dtype=None, activation=None,
-                 flags=0, epsilon=0.0, probability=0.0, strides=None, mode="load"):
+                 flags=0, epsilon=0.0, probability=0.0, experts=None, top_k=0, strides=None, mode="load"):
         if activation not in ACTIVATIONS:
             raise ValueError("activation must be one of %s" % sorted(a for a in ACTIVATIONS if a))
         for t in (dtype, out_dtype, weight_dtype or dtype):
             if t not in OPERATOR_DTYPES:
                 raise ValueError("unknown element type %r" % (t,))
         names = params + results
-        d = HfOperatorDesc(ABI_VERSION, KINDS[kind], m, n, k, OPERATOR_DTYPES[dtype], OPERATOR_DTYPES[out_dtype],
+        extended = kind in EXTENDED_KINDS or experts is not None or flags & BLOCK_SCALES
+        if experts is not None and experts < 1:
+            raise ValueError("experts must be 1 or more")
+        d = HfOperatorDesc(ABI_VERSION, EXTENDED_KINDS[kind] if kind in EXTENDED_KINDS else KINDS[kind], m, n, k, OPERATOR_DTYPES[dtype], OPERATOR_DTYPES[out_dtype],
                            OPERATOR_DTYPES[weight_dtype or dtype], ACTIVATIONS[activation], flags, epsilon,
                            probability)
         for name, v in (strides or {}).items():
@@ -169,8 +193,10 @@ class Operator:
                 raise ValueError("no buffer %r; this operator has %s" % (name, ", ".join(names)))
             d.row_stride[names.index(name)] = v
         h = ctypes.c_void_p()
-        _check(_lib.hf_operator_create(ctypes.byref(d), {"load": 0, "compile": COMPILE_ONLY, "plan": PLAN_ONLY}[mode],
-                                       ctypes.byref(h)))
+        create = _lib.hf_operator_create
+        if extended:
+            d, create = HfOperatorExtendedDesc(d, experts or 0, top_k), _lib.hf_operator_create_extended
+        _check(create(ctypes.byref(d), {"load": 0, "compile": COMPILE_ONLY, "plan": PLAN_ONLY}[mode], ctypes.byref(h)))
         self._h = h
         info = HfOperatorInfo()
         _check(_lib.hf_operator_plan(h, ctypes.byref(info)))
@@ -260,6 +286,12 @@ def _eight(dtype):
     return dtype in ("s8", "f8e4m3")
 
 
+def _block_scales(scales):
+    if scales not in (None, "rows", "blocks"):
+        raise ValueError('scales must be "rows" or "blocks"')
+    return BLOCK_SCALES * (scales == "blocks")
+
+
 class RmsNorm(Operator):
     """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight over each row.
 
@@ -296,15 +328,26 @@ class Matmul(Operator):
 
     params: a [m, k], b [n, k], a_scale [m], b_scale [n] (dtype "s8" or
     "f8e4m3"), bias [n] (bias=True), residual [m, n] (residual=True)
-    results: d [m, n], z [m, n] (save=True: before the activation, for MatmulGrad)"""
+    results: d [m, n], z [m, n] (save=True: before the activation, for MatmulGrad)
+
+    scales="blocks" (dtype "f8e4m3"): a scale for each block of 128 of the
+    contraction, a_scale [ceil(k / 128), m] as BlockQuantize makes it, and
+    b_scale [ceil(n / 128), ceil(k / 128)].
+
+    experts=E: the rows of a are sorted by expert, and rows offsets[e] ..
+    offsets[e + 1] - 1 are multiplied by expert e's weight, rows e * n .. of
+    b [E * n, k]; rows past the last expert's are left as they were.  A parameter
+    offsets (int32 [E + 1], ExpertSort's) follows the scales, which are [E * n]
+    or [E * ceil(n / 128), ceil(k / 128)].  Without bias and residual."""
 
     def __init__(self, m, n, k, dtype="bf16", *, out_dtype=None, bias=False, activation=None, residual=False,
-                 save=False, strides=None, mode="load"):
+                 save=False, scales=None, experts=None, strides=None, mode="load"):
         out_dtype = out_dtype or ("bf16" if _eight(dtype) else dtype)
-        super().__init__("matmul", ["a", "b"] + ["a_scale", "b_scale"] * _eight(dtype) + ["bias"] * bias
+        super().__init__("matmul", ["a", "b"] + ["a_scale", "b_scale"] * _eight(dtype)
+                         + ["offsets"] * (experts is not None) + ["bias"] * bias
                          + ["residual"] * residual, ["d"] + ["z"] * save, m, n, k, dtype, out_dtype,
-                         activation=activation, flags=RESIDUAL * residual + BIAS * bias + SAVE * save,
-                         strides=strides, mode=mode)
+                         activation=activation, flags=RESIDUAL * residual + BIAS * bias + SAVE * save
+                         + _block_scales(scales), experts=experts, strides=strides, mode=mode)
 
 
 class MatmulGrad(Operator):
@@ -312,13 +355,16 @@ class MatmulGrad(Operator):
     gradient before the activation is rounded to dtype on its way into the
     products: a program in f16 scales its loss so that it fits f16's range.
 
-    params: dd [m, n], a [m, k], b [n, k], z [m, n] (with an activation)
-    results: da, db, dbias [n] f32 (bias=True)"""
+    params: dd [m, n], a [m, k], b [n, k], z [m, n] (with an activation),
+    offsets [E + 1] (experts=E: b and db are [E * n, k])
+    results: da, db, dbias [n] f32 (bias=True).  By expert, da's rows past the
+    last expert's are left as they were, and db of an expert without rows is 0."""
 
-    def __init__(self, m, n, k, dtype="bf16", *, bias=False, activation=None, strides=None, mode="load"):
-        super().__init__("matmul_grad", ["dd", "a", "b"] + ["z"] * (ACTIVATIONS.get(activation, 1) != 0),
+    def __init__(self, m, n, k, dtype="bf16", *, bias=False, activation=None, experts=None, strides=None, mode="load"):
+        super().__init__("matmul_grad", ["dd", "a", "b"] + ["z"] * (ACTIVATIONS.get(activation, 1) != 0)
+                         + ["offsets"] * (experts is not None),
                          ["da", "db"] + ["dbias"] * bias, m, n, k, dtype, dtype, activation=activation,
-                         flags=BIAS * bias, strides=strides, mode=mode)
+                         flags=BIAS * bias, experts=experts, strides=strides, mode=mode)
 
 
 class GatedFeedForward(Operator):
@@ -326,26 +372,104 @@ class GatedFeedForward(Operator):
     gate channels' rows, then the n up channels'.
 
     params: a [m, k], b [2n, k], a_scale [m], b_scale [2n] (dtype "s8" or "f8e4m3")
-    results: d [m, n], z [m, 2n] (save=True: both products, for the gradient)"""
+    results: d [m, n], z [m, 2n] (save=True: both products, for the gradient)
 
-    def __init__(self, m, n, k, dtype="bf16", *, out_dtype=None, activation="silu", save=False, strides=None,
-                 mode="load"):
+    scales="blocks" and experts=E as Matmul's: b_scale [2 * ceil(n / 128),
+    ceil(k / 128)], the gate's blocks first; b [E * 2n, k], expert by expert."""
+
+    def __init__(self, m, n, k, dtype="bf16", *, out_dtype=None, activation="silu", save=False, scales=None,
+                 experts=None, strides=None, mode="load"):
         out_dtype = out_dtype or ("bf16" if _eight(dtype) else dtype)
-        super().__init__("gated", ["a", "b"] + ["a_scale", "b_scale"] * _eight(dtype), ["d"] + ["z"] * save,
-                         m, n, k, dtype, out_dtype, activation=activation, flags=SAVE * save, strides=strides,
-                         mode=mode)
+        super().__init__("gated", ["a", "b"] + ["a_scale", "b_scale"] * _eight(dtype)
+                         + ["offsets"] * (experts is not None), ["d"] + ["z"] * save,
+                         m, n, k, dtype, out_dtype, activation=activation, flags=SAVE * save + _block_scales(scales),
+                         experts=experts, strides=strides, mode=mode)
 
 
 class GatedFeedForwardGrad(Operator):
     """The gradient of GatedFeedForward.  The gradients of gate and up are
     rounded to dtype on their way into the products, as MatmulGrad's is.
 
-    params: dd [m, n], a [m, k], b [2n, k], z [m, 2n]
+    params: dd [m, n], a [m, k], b [2n, k], z [m, 2n], offsets [E + 1] (experts=E:
+    b and db are [E * 2n, k])
     results: da [m, k], db [2n, k]"""
 
-    def __init__(self, m, n, k, dtype="bf16", *, activation="silu", strides=None, mode="load"):
-        super().__init__("gated_grad", ["dd", "a", "b", "z"], ["da", "db"], m, n, k, dtype, dtype,
-                         activation=activation, strides=strides, mode=mode)
+    def __init__(self, m, n, k, dtype="bf16", *, activation="silu", experts=None, strides=None, mode="load"):
+        super().__init__("gated_grad", ["dd", "a", "b", "z"] + ["offsets"] * (experts is not None), ["da", "db"],
+                         m, n, k, dtype, dtype, activation=activation, experts=experts, strides=strides, mode=mode)
+
+
+class BlockQuantize(Operator):
+    """Rows in f8e4m3 with a scale for each block of 128 columns, the largest
+    magnitude of a block on 448: x = y * scale, for products with
+    scales="blocks".
+
+    params: x [rows, cols]
+    results: y [rows, cols], scale [ceil(cols / 128), rows] f32"""
+
+    def __init__(self, rows, cols, dtype="bf16", *, strides=None, mode="load"):
+        super().__init__("block_quantize", ["x"], ["y", "scale"], rows, cols, 0, dtype, "f8e4m3", strides=strides,
+                         mode=mode)
+
+
+class ExpertSort(Operator):
+    """The (token, choice) pairs sorted by expert, those of one expert in the
+    order of token * top_k + choice.
+
+    params: expert [tokens, top_k] int32; one outside 0 .. experts - 1 has no row
+    results: place [tokens, top_k] (each pair's row, or -1), order [tokens *
+    top_k] (each row's pair, -1 past the last), offsets [experts + 1] (expert
+    e's rows are offsets[e] .. offsets[e + 1] - 1), all int32"""
+
+    def __init__(self, tokens, top_k, experts, *, strides=None, mode="load"):
+        super().__init__("expert_sort", ["expert"], ["place", "order", "offsets"], tokens, 0, 0, "s32", "s32",
+                         experts=experts, top_k=top_k, strides=strides, mode=mode)
+
+
+class ExpertDispatch(Operator):
+    """y[place[t, j]] = x[t]: every token's row at its pairs' rows by expert.
+    Rows past the last expert's are left as they were.  Its gradient is
+    ExpertCombine with weighted=False.
+
+    params: x [tokens, cols], place [tokens, top_k], x_scale [tokens] (dtype "s8"
+    or "f8e4m3"; scales="blocks": [ceil(cols / 128), tokens])
+    results: y [tokens * top_k, cols], y_scale in the same way"""
+
+    def __init__(self, tokens, top_k, cols, dtype="bf16", *, scales=None, strides=None, mode="load"):
+        super().__init__("expert_dispatch", ["x", "place"] + ["x_scale"] * _eight(dtype),
+                         ["y"] + ["y_scale"] * _eight(dtype), tokens, cols, 0, dtype, dtype,
+                         flags=_block_scales(scales), top_k=top_k, strides=strides, mode=mode)
+
+
+class ExpertCombine(Operator):
+    """d[t] = sum_j weight[t, j] * y[place[t, j]] + residual[t]: the rows by
+    expert back in the tokens' order.  Choices without a row (place -1) add
+    nothing, whatever their weight.
+
+    params: y [tokens * top_k, cols], place [tokens, top_k], weight [tokens,
+    top_k] f32 (weighted=False: none, weights of 1), residual [tokens, cols]
+    (residual=True)
+    results: d [tokens, cols]"""
+
+    def __init__(self, tokens, top_k, cols, dtype="bf16", *, weighted=True, residual=False, strides=None,
+                 mode="load"):
+        super().__init__("expert_combine", ["y", "place"] + ["weight"] * weighted + ["residual"] * residual, ["d"],
+                         tokens, cols, 0, dtype, dtype, flags=RESIDUAL * residual + WEIGHTS * weighted, top_k=top_k,
+                         strides=strides, mode=mode)
+
+
+class ExpertCombineGrad(Operator):
+    """The gradient of a weighted ExpertCombine: dy[place[t, j]] = weight[t, j]
+    * dd[t], dweight[t, j] = <dd[t], y[place[t, j]]>, 0 for a choice without a
+    row.  The residual's gradient is dd itself; without weights the gradient is
+    ExpertDispatch.  dy's rows past the last expert's are left as they were.
+
+    params: dd [tokens, cols], y [tokens * top_k, cols], place, weight
+    results: dy [tokens * top_k, cols], dweight [tokens, top_k] f32"""
+
+    def __init__(self, tokens, top_k, cols, dtype="bf16", *, strides=None, mode="load"):
+        super().__init__("expert_combine_grad", ["dd", "y", "place", "weight"], ["dy", "dweight"], tokens, cols, 0,
+                         dtype, dtype, top_k=top_k, strides=strides, mode=mode)
 
 
 class Dropout(Operator):

@@ -470,6 +470,75 @@ typedef struct {
   int32_t tile_rows, tile_cols, splits;
 } hf_operator_info;
 
+/* ------------------------------------------------------------------------
+ * Operators by expert, and 8-bit products with block scales: the feed-forward
+ * layer of which every token takes a few of many weights.  They are operators
+ * like the ones above, created from a descriptor with two more fields.
+ *
+ * A token has top_k choices; pair p = token * top_k + choice.  Rows "by expert"
+ * are a matrix of tokens * top_k rows, of which rows offsets[e] ..
+ * offsets[e + 1] - 1 are expert e's; rows from offsets[experts] on are no
+ * expert's: they are not read into any result and are left as they were.
+ *
+ * HF_OPERATOR_EXPERT_SORT      pairs sorted by expert, those of one expert in
+ *   the order of p.  An expert outside 0 .. experts - 1 (another rank's) has no
+ *   row: place -1.  order[row] is the row's pair, -1 from offsets[experts] on.
+ *     params  expert [m, top_k] s32
+ *     results place [m, top_k] s32, order [m * top_k] s32, offsets [experts + 1] s32
+ * HF_OPERATOR_EXPERT_DISPATCH  y[place[t, j]] = x[t].
+ *     params  x [m, n] dtype, place [m, top_k] s32, and x_scale [m] f32 (8-bit
+ *             dtype) or [ceil(n / 128), m] f32 (BLOCK_SCALES)
+ *     results y [m * top_k, n], y_scale [m * top_k] or [ceil(n / 128), m * top_k]
+ * HF_OPERATOR_EXPERT_COMBINE   d[t] = sum_j weight[t, j] * y[place[t, j]]
+ *   + residual[t], in the order of j; choices without a row add nothing.
+ *   Without WEIGHTS, weights of 1: the gradient of a dispatch.
+ *     params  y [m * top_k, n], place [m, top_k] s32, weight [m, top_k] f32
+ *             (WEIGHTS), residual [m, n] (RESIDUAL)
+ *     results d [m, n]
+ * HF_OPERATOR_EXPERT_COMBINE_GRAD  dy[place[t, j]] = weight[t, j] * dd[t];
+ *   dweight[t, j] = <dd[t], y[place[t, j]]>, 0 for a choice without a row.  The
+ *   residual's gradient is dd itself.
+ *     params  dd [m, n], y [m * top_k, n], place [m, top_k] s32, weight [m, top_k] f32
+ *     results dy [m * top_k, n], dweight [m, top_k] f32
+ * HF_OPERATOR_BLOCK_QUANTIZE   each row's blocks of 128 columns in f8e4m3: scale
+ *   = max|x| / 448 of the block, y = round(x / scale), 0 in a block of zeros.  A
+ *   block that holds a NaN has scale NaN.
+ *     params  x [m, n] dtype
+ *     results y [m, n] f8e4m3, scale [ceil(n / 128), m] f32
+ * HF_OPERATOR_MATMUL, _GATED and their gradients with experts > 0: rows by
+ *   expert, b holds the experts' weights one after another ([experts * n, k],
+ *   gated [experts * 2n, k], an expert's gate rows before its up rows; b_scale
+ *   alike).  A parameter offsets [experts + 1] s32 follows b's scales (in a
+ *   gradient: z).  db of an expert without rows is 0.  No bias, no residual.
+ * HF_OPERATOR_MATMUL, _GATED with BLOCK_SCALES (f8e4m3): z[m, n] = sum over
+ *   blocks c of a_scale[c, m] * b_scale[n / 128, c] * the block's sum of a * b.
+ *     params  a_scale [ceil(k / 128), m], b_scale [ceil(n / 128), ceil(k / 128)]
+ *             f32 (gated: the gate's ceil(n / 128) rows, then the up half's; by
+ *             expert: one such array after another)
+ *
+ * place and offsets are read on the GPU.  Whatever they hold, no access leaves
+ * its buffer, but results are defined only for those of a sort (or of equal
+ * meaning: offsets that do not decrease, places of which no two are equal).
+ * dtype: bf16, f16 and f32 for the rows; dispatch also s8 and f8e4m3; products
+ * as above.  The sort takes dtype and out_dtype of any type and uses neither;
+ * dispatch, combine and its gradient take out_dtype = dtype, the quantizer
+ * HF_F8E4M3. */
+#define HF_OPERATOR_EXPERT_SORT 7
+#define HF_OPERATOR_EXPERT_DISPATCH 8
+#define HF_OPERATOR_EXPERT_COMBINE 9
+#define HF_OPERATOR_EXPERT_COMBINE_GRAD 10
+#define HF_OPERATOR_BLOCK_QUANTIZE 11
+
+#define HF_OPERATOR_WEIGHTS 8u
+#define HF_OPERATOR_BLOCK_SCALES 16u
+#define HF_MAX_EXPERTS 1024 /* and choices of a token */
+
+typedef struct {
+  hf_operator_desc op;       /* kind: any of the above too */
+  int64_t experts;           /* the sort, and products by expert; else 0 */
+  int64_t top_k;             /* the sort, dispatch, combine and its gradient; else 0 */
+} hf_operator_extended_desc;
+
 typedef struct hf_operator hf_operator;
 
 /* Validate and plan.  flags: 0, or HF_CREATE_PLAN_ONLY /
@@ -478,6 +547,10 @@ typedef struct hf_operator hf_operator;
  * stride of 8 MB or more in a product's operand, and a product of more tiles
  * than a launch holds: never below 2^37 sums), HF_ERR_HIP, HF_ERR_NOMEM. */
 hf_status hf_operator_create(const hf_operator_desc *desc, uint32_t flags, hf_operator **out);
+
+/* The same from an extended descriptor, which may be any operator's.  Errors
+ * also: more than HF_MAX_EXPERTS experts, 2^31 - 2^20 pairs or more. */
+hf_status hf_operator_create_extended(const hf_operator_extended_desc *desc, uint32_t flags, hf_operator **out);
 
 /* Copy the plan into *info. */
 hf_status hf_operator_plan(const hf_operator *op, hf_operator_info *info);
