@@ -196,38 +196,42 @@ struct StepS8 {
   static __device__ __forceinline__ f32x4 bits(Acc c) { return __builtin_bit_cast(f32x4, c); }
 };
 
-// A block's scale as m 2^e, m in [1, 2) (or 0, infinite, NaN; small for a
+// e4m3 with block scales: a step is one block of 128 of the contraction, whose
+// sum comes out of the matrix instruction by itself and is then added with its
+// two scales.  A scale is m 2^e, m in [1, 2) (or 0, infinite, NaN; small for a
 // denormal): e goes into the matrix instruction as its own block scale (e8m0,
-// 127 + e), which leaves the product of two m's, in [1, 4), to the vector
-// unit.  The product of two whole scales might leave f32's range where the
-// sums are in it.
-struct BlockScale {
-  float m;
-  int e;
-  BlockScale() = default;
-  __device__ __forceinline__ explicit BlockScale(float s) {
-    const int p = min(max(__builtin_amdgcn_frexp_expf(s) - 1, -127), 127);
-    m = __builtin_ldexpf(s, -p);
-    e = p + 127;
-  }
-  __device__ __forceinline__ float whole() const { return __builtin_ldexpf(m, e - 127); }
-};
-// e4m3 with block scales: a step is one block of 128 of the contraction.  Its
-// sum comes out of the matrix instruction and is added with the mantissas'
-// factor: four multiply-adds a lane beside an instruction of 32 cycles.
+// 127 + e), which leaves the product of two m's, in [1, 4), to the vector unit:
+// four multiply-adds a lane beside an instruction of 32 cycles.  The product of
+// two whole scales might leave f32's range where the sums are in it, and two
+// factors would cost four more operations.
 struct StepF8Block {
   typedef f32x4 Acc;
   static constexpr bool kBlock = true;
   static constexpr bool kWide = false;
   static constexpr int kBytes = 1;
-  static constexpr int kSteps = 1;
-  static __device__ __forceinline__ Acc add(const i32x4 (&a)[2], const i32x4 (&b)[2], BlockScale sa, BlockScale sb, Acc c) {
+  struct Scale {  // of a row of a and a block of b
+    float m;
+    int ea, eb;
+  };
+  static __device__ __forceinline__ float split(float s, int &e) {
+    const int p = min(max(__builtin_amdgcn_frexp_expf(s) - 1, -127), 127);
+    e = p + 127;
+    return __builtin_ldexpf(s, -p);
+  }
+  static __device__ __forceinline__ Scale scale(float a, float b) {
+    Scale s;
+    const float m = split(b, s.eb);
+    s.m = split(a, s.ea) * m;
+    return s;
+  }
+  static __device__ __forceinline__ f32x4 block(const i32x4 (&a)[2], const i32x4 (&b)[2], Scale s) {
     const i32x8 x = __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7);
     const i32x8 y = __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7);
-    const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0, 0, 0, 0}, 0, 0, 0, sb.e, 0, sa.e);
-    const float f = sa.m * sb.m;
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0, 0, 0, 0}, 0, 0, 0, s.eb, 0, s.ea);
+  }
+  static __device__ __forceinline__ Acc add(Acc c, f32x4 t, Scale s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i], f, c[i]);
+    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i], s.m, c[i]);
     return c;
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
@@ -239,14 +243,19 @@ struct StepF8BlockWide {
   static constexpr bool kBlock = true;
   static constexpr bool kWide = true;
   static constexpr int kBytes = 1;
-  static constexpr int kSteps = 2;
-  static __device__ __forceinline__ Acc add(const i32x4 (&a)[2], const i32x4 (&b)[2], BlockScale sa, BlockScale sb, Acc c) {
+  struct Scale {
+    float a, b;
+  };
+  static __device__ __forceinline__ Scale scale(float a, float b) { return Scale{a, b}; }
+  static __device__ __forceinline__ f32x4 block(const i32x4 (&a)[2], const i32x4 (&b)[2], Scale) {
     f32x4 t = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k) t = StepF8Wide::step(a, b, t, k);
-    const float p = sa.whole(), q = sb.whole();
+    return t;
+  }
+  static __device__ __forceinline__ Acc add(Acc c, f32x4 t, Scale s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i] * p, q, c[i]);
+    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i] * s.a, s.b, c[i]);
     return c;
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
@@ -269,5 +278,22 @@ __device__ __forceinline__ typename Step::Acc mma(const i32x4 (&a)[2], const i32
   for (int k = 0; k < Step::kSteps; ++k) c = Step::step(a, b, c, k);
   return c;
 }
+template <class Step>
+__device__ __forceinline__ typename Step::Acc mma_block(const i32x4 (&a)[2], const i32x4 (&b)[2], float sa, float sb,
+                                                        typename Step::Acc c) {
+  const typename Step::Scale s = Step::scale(sa, sb);
+  return Step::add(c, Step::block(a, b, s), s);
+}
+
+// What a Step without block scales has in the place of a scale.
+struct NoScale {};
+template <class Step, bool = Step::kBlock>
+struct ScaleOf {
+  typedef NoScale Type;
+};
+template <class Step>
+struct ScaleOf<Step, true> {
+  typedef typename Step::Scale Type;
+};
 
 }  // namespace hf

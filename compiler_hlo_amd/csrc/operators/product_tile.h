@@ -283,33 +283,37 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   // Past the last stage they are zeros, as the operands are.
   constexpr bool BLOCK = Step::kBlock;
   const uint32_t scales = base + 2 * kStage;
-  const int64_t block0 = (int64_t)k0;
-  auto fetch_scales = [&](int kt) {
-    if constexpr (BLOCK) {
-      const int u = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-      const bool rows = u < WAVES / 2;
-      const float *from;
-      if (rows) {
-        from = a.a_scale + (block0 + kt) * a.lda_scale + m0;
-      } else {
-        const int half = (u - WAVES / 2) / (WAVES / 4);
-        const int n = gated ? n0 : n0 + half * HN;
-        from = a.b_scale + (min(n, a.n - 1) / 128 + (gated ? half * a.b_scale_half : 0)) * a.ldb_scale + block0 + kt;
-      }
-      const uint32_t v = (rows ? threadIdx.x : threadIdx.x % 64) * 4;
-      load_to_lds4(scales + (kt & 3) * S::kScale + u * 256, view((const char *)from, kt >= kn ? 0 : rows ? (a.m - m0) * 4 : 4),
-                   v);
+  // Where a wave's lie is chosen here: the loop has no branch, or the compiler
+  // moves products past the barriers.
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const char *scale_from = nullptr;
+  int64_t scale_step = 0;
+  int scale_bytes = 0;
+  const uint32_t scale_lane = (wave < WAVES / 2 ? threadIdx.x : threadIdx.x % 64) * 4;
+  if constexpr (BLOCK) {
+    if (wave < WAVES / 2) {
+      scale_from = (const char *)(a.a_scale + (int64_t)k0 * a.lda_scale + m0);
+      scale_step = a.lda_scale * 4;
+      scale_bytes = (a.m - m0) * 4;
+    } else {
+      const int half = (wave - WAVES / 2) / (WAVES / 4), n = gated ? n0 : n0 + half * HN;
+      scale_from = (const char *)(a.b_scale + (min(n, a.n - 1) / 128 + (gated ? half * a.b_scale_half : 0)) * a.ldb_scale + k0);
+      scale_step = scale_bytes = 4;
     }
+  }
+  auto fetch_scales = [&](int kt) {
+    if constexpr (BLOCK)
+      load_to_lds4(scales + (kt & 3) * S::kScale + wave * 256, view(scale_from + kt * scale_step, kt < kn ? scale_bytes : 0),
+                   scale_lane);
   };
-  BlockScale sa[TM], sb[2];
-  auto read_scales = [&](int kt, int h) {
+  typename ScaleOf<Step>::Type scale[TM];
+  auto read_scales = [&](int kt, int h, int j) {
     if constexpr (BLOCK) {
       const uint32_t at = scales + (kt & 3) * S::kScale;
+      const float b = lds_float(at + (WAVES / 2 + j * (WAVES / 4)) * 256);
 #pragma unroll
       for (int x = 0; x < TM; ++x)
-        sa[x] = BlockScale(lds_float(at + (h * HM + wm * (HM / 2) + x * 16 + (threadIdx.x & 15)) * 4));
-#pragma unroll
-      for (int j = 0; j < 2; ++j) sb[j] = BlockScale(lds_float(at + (WAVES / 2 + j * (WAVES / 4)) * 256));
+        scale[x] = Step::scale(lds_float(at + (h * HM + wm * (HM / 2) + x * 16 + (threadIdx.x & 15)) * 4), b);
     }
   };
   // the second stage is beyond the 16 bits of a read's constant offset: its
@@ -338,10 +342,20 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   auto multiply = [&](int i, int j) {
     __builtin_amdgcn_s_setprio(1);
     if constexpr (BLOCK) {
+      // a block's sum is added while the second after it is multiplied, by
+      // when it is there; the barriers keep three of them in registers, not all
+      constexpr int kBlocks = TM * TN;
+      f32x4 t[3];
 #pragma unroll
-      for (int y = 0; y < TN; ++y)
-#pragma unroll
-        for (int x = 0; x < TM; ++x) acc[i][j][x][y] = Step::add(fa[x], fb[j][y], sa[x], sb[j], acc[i][j][x][y]);
+      for (int n = 0; n < kBlocks + 2; ++n) {
+        if (n < kBlocks) t[n % 3] = Step::block(fa[n % TM], fb[j][n / TM], scale[n % TM]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (n >= 2) {
+          const int x = (n - 2) % TM, y = (n - 2) / TM;
+          acc[i][j][x][y] = Step::add(acc[i][j][x][y], t[(n - 2) % 3], scale[x]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < Step::kSteps; ++k)
@@ -391,15 +405,15 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
     meet();
     if (WAVES == 8 && wm) meet();
     for (int kt = 0; kt < kn; kt += 2) {
-      quarter([&] { read_a(0, 0), read_scales(kt, 0); }, [&] { fetch_scales(kt + 2), fetch_b(kt + 2, 0, 0); }, 0, 0);
-      quarter([&] { read_b(0, 1); }, [&] { fetch_a(kt + 2, 0, 0); }, 0, 1);
-      quarter([&] { read_a(0, 1), read_scales(kt, 1); }, [&] { fetch_b(kt + 2, 0, 1); }, 1, 1);
-      quarter([&] { read_b(1, 1); }, [&] { fetch_a(kt + 2, 0, 1); }, 1, 0);
+      quarter([&] { read_a(0, 0), read_scales(kt, 0, 0); }, [&] { fetch_scales(kt + 2), fetch_b(kt + 2, 0, 0); }, 0, 0);
+      quarter([&] { read_b(0, 1), read_scales(kt, 0, 1); }, [&] { fetch_a(kt + 2, 0, 0); }, 0, 1);
+      quarter([&] { read_a(0, 1), read_scales(kt, 1, 1); }, [&] { fetch_b(kt + 2, 0, 1); }, 1, 1);
+      quarter([&] { read_b(1, 1), read_scales(kt, 1, 0); }, [&] { fetch_a(kt + 2, 0, 1); }, 1, 0);
       // an odd number of stages: the last is all zeros and adds nothing
-      quarter([&] { read_a(1, 0), read_scales(kt + 1, 0); }, [&] { fetch_scales(kt + 3), fetch_b(kt + 3, 1, 1); }, 0, 1);
-      quarter([&] { read_b(1, 0); }, [&] { fetch_a(kt + 3, 1, 0); }, 0, 0);
-      quarter([&] { read_a(1, 1), read_scales(kt + 1, 1); }, [&] { fetch_b(kt + 3, 1, 0); }, 1, 0);
-      quarter([&] { read_b(0, 0); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 1);
+      quarter([&] { read_a(1, 0), read_scales(kt + 1, 0, 1); }, [&] { fetch_scales(kt + 3), fetch_b(kt + 3, 1, 1); }, 0, 1);
+      quarter([&] { read_b(1, 0), read_scales(kt + 1, 0, 0); }, [&] { fetch_a(kt + 3, 1, 0); }, 0, 0);
+      quarter([&] { read_a(1, 1), read_scales(kt + 1, 1, 0); }, [&] { fetch_b(kt + 3, 1, 0); }, 1, 0);
+      quarter([&] { read_b(0, 0), read_scales(kt + 1, 1, 1); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 1);
     }
     if (WAVES == 8 && !wm) meet();
     // nothing may still be on its way to LDS when its bytes are used again
@@ -526,16 +540,14 @@ __device__ __forceinline__ void strip_tile(const ProductArgs &a, int strip, int 
     const uint32_t at = stage * kStage;
     i32x4 fb[2];
     HB::read<1>(pb, at, 0, fb);
-    BlockScale sb;
-    if (BLOCK) sb = BlockScale(lds_float(scales + stage * Strip<Step>::kScale + 256));
+    const float sb = BLOCK ? lds_float(scales + stage * Strip<Step>::kScale + 256) : 0.f;
 #pragma unroll
     for (int x = 0; x < TM; ++x) {
       if (x * 16 >= a.m) break;
       i32x4 fa[2];
       HA::read<TM>(pa, at, x, fa);
       if constexpr (BLOCK)
-        acc[x] = Step::add(fa, fb, BlockScale(lds_float(scales + stage * Strip<Step>::kScale + (x * 16 + (l & 15)) * 4)), sb,
-                           acc[x]);
+        acc[x] = mma_block<Step>(fa, fb, lds_float(scales + stage * Strip<Step>::kScale + (x * 16 + (l & 15)) * 4), sb, acc[x]);
       else
         acc[x] = mma<Step>(fa, fb, acc[x]);
     }

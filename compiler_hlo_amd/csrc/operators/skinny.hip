@@ -72,7 +72,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
         if constexpr (BLOCK)
-          acc[h] = Step::add(f.a[q], f.b[h][q], BlockScale(f.sa[q]), BlockScale(f.sb[h][q]), acc[h]);
+          acc[h] = mma_block<Step>(f.a[q], f.b[h][q], f.sa[q], f.sb[h][q], acc[h]);
         else
           acc[h] = mma<Step>(f.a[q], f.b[h][q], acc[h]);
       }
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_kernel(SkinnyArgs s) {
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
         if constexpr (BLOCK)
-          acc[h] = Step::add(fa, fb[h], BlockScale(scale_a(c)), BlockScale(scale_b(h, c)), acc[h]);
+          acc[h] = mma_block<Step>(fa, fb[h], scale_a(c), scale_b(h, c), acc[h]);
         else
           acc[h] = mma<Step>(fa, fb[h], acc[h]);
       }
