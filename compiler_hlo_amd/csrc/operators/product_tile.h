@@ -289,7 +289,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   const char *scale_from = nullptr;
   int64_t scale_step = 0;
   int scale_bytes = 0;
-  const uint32_t scale_lane = (wave < WAVES / 2 ? threadIdx.x : threadIdx.x % 64) * 4;
+  const uint32_t scale_lane = wave < WAVES / 2 ? threadIdx.x * 4 : 0;
   if constexpr (BLOCK) {
     if (wave < WAVES / 2) {
       scale_from = (const char *)(a.a_scale + (int64_t)k0 * a.lda_scale + m0);
@@ -306,14 +306,24 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
       load_to_lds4(scales + (kt & 3) * S::kScale + wave * 256, view(scale_from + kt * scale_step, kt < kn ? scale_bytes : 0),
                    scale_lane);
   };
+  // A quarter's scales are read from LDS a quarter ahead, so that what is done
+  // with them goes on while the operands are on their way.  One address serves
+  // all: b's scale lies there once for every lane.
   typename ScaleOf<Step>::Type scale[TM];
-  auto read_scales = [&](int kt, int h, int j) {
+  float rows_scale[BLOCK ? TM : 1], b_scale = 0.f;
+  const uint32_t scale_at = scales + (wm * (HM / 2) + (threadIdx.x & 15)) * 4;
+  auto ask_scales = [&](int kt, int h, int j) {
     if constexpr (BLOCK) {
-      const uint32_t at = scales + (kt & 3) * S::kScale;
-      const float b = lds_float(at + (WAVES / 2 + j * (WAVES / 4)) * 256);
+      const uint32_t at = scale_at + (kt & 3) * S::kScale;
+      b_scale = lds_float(at + (WAVES / 2 + j * (WAVES / 4)) * 256);
 #pragma unroll
-      for (int x = 0; x < TM; ++x)
-        scale[x] = Step::scale(lds_float(at + (h * HM + wm * (HM / 2) + x * 16 + (threadIdx.x & 15)) * 4), b);
+      for (int x = 0; x < TM; ++x) rows_scale[x] = lds_float(at + (h * HM + x * 16) * 4);
+    }
+  };
+  auto take_scales = [&] {
+    if constexpr (BLOCK) {
+#pragma unroll
+      for (int x = 0; x < TM; ++x) scale[x] = Step::scale(rows_scale[x], b_scale);
     }
   };
   // the second stage is beyond the 16 bits of a read's constant offset: its
@@ -339,21 +349,30 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
 #pragma unroll
     for (int y = 0; y < TN; ++y) HB::template read<TN>(pb[odd], h * HB::kBytes, y, fb[h][y]);
   };
+  constexpr int kBlocks = TM * TN, kLate = 4;
+  f32x4 late[BLOCK ? kLate : 1];
+  auto add_block = [&](int i, int j, int n) {
+    if constexpr (BLOCK) {
+      const int x = n % TM, y = n / TM;
+      acc[i][j][x][y] = Step::add(acc[i][j][x][y], late[n % kLate], scale[x]);
+    }
+  };
+  auto settle = [&](int i, int j) {
+    if constexpr (BLOCK) {
+#pragma unroll
+      for (int n = kBlocks - kLate; n < kBlocks; ++n) add_block(i, j, n);
+    }
+  };
   auto multiply = [&](int i, int j) {
     __builtin_amdgcn_s_setprio(1);
     if constexpr (BLOCK) {
-      // a block's sum is added while the second after it is multiplied, by
-      // when it is there; the barriers keep three of them in registers, not all
-      constexpr int kBlocks = TM * TN;
-      f32x4 t[3];
+      // A block's sum is added after three more are asked for, by when it is
+      // there; the last ones wait until the other wave has its turn (settle).
 #pragma unroll
-      for (int n = 0; n < kBlocks + 2; ++n) {
-        if (n < kBlocks) t[n % 3] = Step::block(fa[n % TM], fb[j][n / TM], scale[n % TM]);
+      for (int n = 0; n < kBlocks; ++n) {
+        if (n >= kLate) add_block(i, j, n - kLate);
         __builtin_amdgcn_sched_barrier(0);
-        if (n >= 2) {
-          const int x = (n - 2) % TM, y = (n - 2) / TM;
-          acc[i][j][x][y] = Step::add(acc[i][j][x][y], t[(n - 2) % 3], scale[x]);
-        }
+        late[n % kLate] = Step::block(fa[n % TM], fb[j][n / TM], scale[n % TM]);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -385,8 +404,15 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   // (With block scales every stage asks for one more, at its first quarter: six
   // quarters hold one or two of those.)
   constexpr int kAhead = 3 * (HA::kLoads + HB::kLoads) + (BLOCK ? 1 : 0);
-  auto quarter = [&](auto read, auto fetch, int i, int j) {
+  // was_i, was_j: the quarter before; kt, next_i, next_j: the one after
+  auto quarter = [&](auto read, auto fetch, int was_i, int was_j, int i, int j, int kt, int next_i, int next_j) {
     read();
+    if constexpr (BLOCK) {
+      __builtin_amdgcn_sched_barrier(0);
+      settle(was_i, was_j);
+      take_scales();
+      ask_scales(kt, next_i, next_j);
+    }
     fetch();
     arrived<kAhead>();
     meet();
@@ -401,20 +427,28 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
     arrived<kAhead>();
     meet();
     read_b(0, 0);
+    ask_scales(0, 0, 0);
+    if constexpr (BLOCK) {  // no quarter was before the first
+#pragma unroll
+      for (int n = 0; n < kLate; ++n) late[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < TM; ++x) scale[x] = Step::scale(0.f, 0.f);
+    }
     arrived<kAhead>();
     meet();
     if (WAVES == 8 && wm) meet();
     for (int kt = 0; kt < kn; kt += 2) {
-      quarter([&] { read_a(0, 0), read_scales(kt, 0, 0); }, [&] { fetch_scales(kt + 2), fetch_b(kt + 2, 0, 0); }, 0, 0);
-      quarter([&] { read_b(0, 1), read_scales(kt, 0, 1); }, [&] { fetch_a(kt + 2, 0, 0); }, 0, 1);
-      quarter([&] { read_a(0, 1), read_scales(kt, 1, 1); }, [&] { fetch_b(kt + 2, 0, 1); }, 1, 1);
-      quarter([&] { read_b(1, 1), read_scales(kt, 1, 0); }, [&] { fetch_a(kt + 2, 0, 1); }, 1, 0);
+      quarter([&] { read_a(0, 0); }, [&] { fetch_scales(kt + 2), fetch_b(kt + 2, 0, 0); }, 1, 1, 0, 0, kt, 0, 1);
+      quarter([&] { read_b(0, 1); }, [&] { fetch_a(kt + 2, 0, 0); }, 0, 0, 0, 1, kt, 1, 1);
+      quarter([&] { read_a(0, 1); }, [&] { fetch_b(kt + 2, 0, 1); }, 0, 1, 1, 1, kt, 1, 0);
+      quarter([&] { read_b(1, 1); }, [&] { fetch_a(kt + 2, 0, 1); }, 1, 1, 1, 0, kt + 1, 0, 1);
       // an odd number of stages: the last is all zeros and adds nothing
-      quarter([&] { read_a(1, 0), read_scales(kt + 1, 0, 1); }, [&] { fetch_scales(kt + 3), fetch_b(kt + 3, 1, 1); }, 0, 1);
-      quarter([&] { read_b(1, 0), read_scales(kt + 1, 0, 0); }, [&] { fetch_a(kt + 3, 1, 0); }, 0, 0);
-      quarter([&] { read_a(1, 1), read_scales(kt + 1, 1, 0); }, [&] { fetch_b(kt + 3, 1, 0); }, 1, 0);
-      quarter([&] { read_b(0, 0), read_scales(kt + 1, 1, 1); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 1);
+      quarter([&] { read_a(1, 0); }, [&] { fetch_scales(kt + 3), fetch_b(kt + 3, 1, 1); }, 1, 0, 0, 1, kt + 1, 0, 0);
+      quarter([&] { read_b(1, 0); }, [&] { fetch_a(kt + 3, 1, 0); }, 0, 1, 0, 0, kt + 1, 1, 0);
+      quarter([&] { read_a(1, 1); }, [&] { fetch_b(kt + 3, 1, 0); }, 0, 0, 1, 0, kt + 1, 1, 1);
+      quarter([&] { read_b(0, 0); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 0, 1, 1, kt + 2, 0, 0);
     }
+    settle(1, 1);
     if (WAVES == 8 && !wm) meet();
     // nothing may still be on its way to LDS when its bytes are used again
     arrived<0>();
