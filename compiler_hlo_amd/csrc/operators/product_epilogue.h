@@ -198,12 +198,13 @@ struct StepS8 {
 
 // e4m3 with block scales: a step is one block of 128 of the contraction, whose
 // sum comes out of the matrix instruction by itself and is then added with its
-// two scales.  A scale is m 2^e, m in [1, 2) (or 0, infinite, NaN; small for a
-// denormal): e goes into the matrix instruction as its own block scale (e8m0,
-// 127 + e), which leaves the product of two m's, in [1, 4), to the vector unit:
-// four multiply-adds a lane beside an instruction of 32 cycles.  The product of
-// two whole scales might leave f32's range where the sums are in it, and two
-// factors would cost four more operations.
+// two scales: four multiply-adds a lane beside an instruction of 32 cycles.
+// The product of the two scales might leave f32's range where the sums are in
+// it, and two factors would cost four more operations.  So b's scale is taken
+// as m 2^e with e within +-64, where a block's sum times 2^e (the matrix
+// instruction's own block scale, e8m0) is in range, and a's scale times m is
+// the factor: m is in [1, 2), and beyond e's bounds it goes on towards b's
+// scale, so that the factor leaves the range only where the sum does.
 struct StepF8Block {
   typedef f32x4 Acc;
   static constexpr bool kBlock = true;
@@ -211,23 +212,16 @@ struct StepF8Block {
   static constexpr int kBytes = 1;
   struct Scale {  // of a row of a and a block of b
     float m;
-    int ea, eb;
+    int e;
   };
-  static __device__ __forceinline__ float split(float s, int &e) {
-    const int p = min(max(__builtin_amdgcn_frexp_expf(s) - 1, -127), 127);
-    e = p + 127;
-    return __builtin_ldexpf(s, -p);
-  }
   static __device__ __forceinline__ Scale scale(float a, float b) {
-    Scale s;
-    const float m = split(b, s.eb);
-    s.m = split(a, s.ea) * m;
-    return s;
+    const int e = min(max(__builtin_amdgcn_frexp_expf(b) - 1, -64), 64);
+    return Scale{a * __builtin_ldexpf(b, -e), e + 127};
   }
   static __device__ __forceinline__ f32x4 block(const i32x4 (&a)[2], const i32x4 (&b)[2], Scale s) {
     const i32x8 x = __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7);
     const i32x8 y = __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0, 0, 0, 0}, 0, 0, 0, s.eb, 0, s.ea);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0, 0, 0, 0}, 0, 0, 0, s.e, 0, 0x7f);
   }
   static __device__ __forceinline__ Acc add(Acc c, f32x4 t, Scale s) {
 #pragma unroll

@@ -349,28 +349,24 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
 #pragma unroll
     for (int y = 0; y < TN; ++y) HB::template read<TN>(pb[odd], h * HB::kBytes, y, fb[h][y]);
   };
+  // Block scales: the sum of block n of a quarter is added kLate blocks later,
+  // by when it is there, the last ones' between the next quarter's first.
   constexpr int kBlocks = TM * TN, kLate = 4;
   f32x4 late[BLOCK ? kLate : 1];
-  auto add_block = [&](int i, int j, int n) {
+  auto add_block = [&](int i, int j, int n, const auto &by) {
     if constexpr (BLOCK) {
       const int x = n % TM, y = n / TM;
-      acc[i][j][x][y] = Step::add(acc[i][j][x][y], late[n % kLate], scale[x]);
+      acc[i][j][x][y] = Step::add(acc[i][j][x][y], late[n % kLate], by[x]);
     }
   };
-  auto settle = [&](int i, int j) {
-    if constexpr (BLOCK) {
-#pragma unroll
-      for (int n = kBlocks - kLate; n < kBlocks; ++n) add_block(i, j, n);
-    }
-  };
-  auto multiply = [&](int i, int j) {
+  typename ScaleOf<Step>::Type was[TM];
+  auto multiply = [&](int was_i, int was_j, int i, int j) {
     __builtin_amdgcn_s_setprio(1);
     if constexpr (BLOCK) {
-      // A block's sum is added after three more are asked for, by when it is
-      // there; the last ones wait until the other wave has its turn (settle).
 #pragma unroll
       for (int n = 0; n < kBlocks; ++n) {
-        if (n >= kLate) add_block(i, j, n - kLate);
+        if (n >= kLate) add_block(i, j, n - kLate, scale);
+        else if (n > 0) add_block(was_i, was_j, kBlocks - kLate + n, was);
         __builtin_amdgcn_sched_barrier(0);
         late[n % kLate] = Step::block(fa[n % TM], fb[j][n / TM], scale[n % TM]);
         __builtin_amdgcn_sched_barrier(0);
@@ -409,14 +405,16 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
     read();
     if constexpr (BLOCK) {
       __builtin_amdgcn_sched_barrier(0);
-      settle(was_i, was_j);
+      add_block(was_i, was_j, kBlocks - kLate, scale);
+#pragma unroll
+      for (int x = 0; x < TM; ++x) was[x] = scale[x];
       take_scales();
       ask_scales(kt, next_i, next_j);
     }
     fetch();
     arrived<kAhead>();
     meet();
-    multiply(i, j);
+    multiply(was_i, was_j, i, j);
     meet();
   };
   if (kn > 0) {
@@ -448,7 +446,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
       quarter([&] { read_a(1, 1); }, [&] { fetch_b(kt + 3, 1, 0); }, 0, 0, 1, 0, kt + 1, 1, 1);
       quarter([&] { read_b(0, 0); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 0, 1, 1, kt + 2, 0, 0);
     }
-    settle(1, 1);
+#pragma unroll
+    for (int n = kBlocks - kLate; n < kBlocks; ++n) add_block(1, 1, n, scale);
     if (WAVES == 8 && !wm) meet();
     // nothing may still be on its way to LDS when its bytes are used again
     arrived<0>();
