@@ -47,10 +47,11 @@ __device__ __forceinline__ float lds_float(uint32_t at) {
   return *(const __attribute__((address_space(3))) float *)(uintptr_t)at;
 }
 
-// All loads but the newest N have arrived, and this wave's LDS reads.
-template <int N>
+// All loads but the newest N have arrived, and this wave's LDS reads (but the
+// newest READS of them).
+template <int N, int READS = 0>
 __device__ __forceinline__ void arrived() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(%1)" : : "n"(N), "n"(READS) : "memory");
 }
 
 // A barrier that nothing is moved across; it waits for no memory by itself.
@@ -306,10 +307,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
       load_to_lds4(scales + (kt & 3) * S::kScale + wave * 256, view(scale_from + kt * scale_step, kt < kn ? scale_bytes : 0),
                    scale_lane);
   };
-  // A quarter's scales are read from LDS a quarter ahead, so that what is done
-  // with them goes on while the operands are on their way.  One address serves
-  // all: b's scale lies there once for every lane.
-  typename ScaleOf<Step>::Type scale[TM];
+  // A quarter's scales are read from LDS a quarter ahead, and made into factors
+  // between that quarter's products.  One address serves all: b's scale lies
+  // there once for every lane.
+  typename ScaleOf<Step>::Type scale[TM], next[TM];
   float rows_scale[BLOCK ? TM : 1], b_scale = 0.f;
   const uint32_t scale_at = scales + (wm * (HM / 2) + (threadIdx.x & 15)) * 4;
   auto ask_scales = [&](int kt, int h, int j) {
@@ -318,12 +319,6 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
       b_scale = lds_float(at + (WAVES / 2 + j * (WAVES / 4)) * 256);
 #pragma unroll
       for (int x = 0; x < TM; ++x) rows_scale[x] = lds_float(at + (h * HM + x * 16) * 4);
-    }
-  };
-  auto take_scales = [&] {
-    if constexpr (BLOCK) {
-#pragma unroll
-      for (int x = 0; x < TM; ++x) scale[x] = Step::scale(rows_scale[x], b_scale);
     }
   };
   // the second stage is beyond the 16 bits of a read's constant offset: its
@@ -349,37 +344,46 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
 #pragma unroll
     for (int y = 0; y < TN; ++y) HB::template read<TN>(pb[odd], h * HB::kBytes, y, fb[h][y]);
   };
-  // Block scales: the sum of block n of a quarter is added kLate blocks later,
-  // by when it is there, the last ones' between the next quarter's first.
+  // Block scales: the sum of block n of a quarter is added after kLate more are
+  // asked for, by when it is there; the last ones' while the other wave has its
+  // turn.  (A matrix instruction takes 32 cycles, 34 with two vector
+  // instructions behind it and 40 with four, so a quarter's additions are
+  // divided between the two sections.)
   constexpr int kBlocks = TM * TN, kLate = 4;
   f32x4 late[BLOCK ? kLate : 1];
-  auto add_block = [&](int i, int j, int n, const auto &by) {
+  auto add_block = [&](int i, int j, int n) {
     if constexpr (BLOCK) {
       const int x = n % TM, y = n / TM;
-      acc[i][j][x][y] = Step::add(acc[i][j][x][y], late[n % kLate], by[x]);
+      acc[i][j][x][y] = Step::add(acc[i][j][x][y], late[n % kLate], scale[x]);
     }
   };
-  typename ScaleOf<Step>::Type was[TM];
-  auto multiply = [&](int was_i, int was_j, int i, int j) {
-    __builtin_amdgcn_s_setprio(1);
+  auto settle = [&](int i, int j) {
+#pragma unroll
+    for (int n = kBlocks - kLate; n < kBlocks; ++n) add_block(i, j, n);
+  };
+  auto multiply = [&](int i, int j) {
     if constexpr (BLOCK) {
 #pragma unroll
       for (int n = 0; n < kBlocks; ++n) {
-        if (n >= kLate) add_block(i, j, n - kLate, scale);
-        else if (n > 0) add_block(was_i, was_j, kBlocks - kLate + n, was);
+        if (n >= kLate) add_block(i, j, n - kLate);
+        if (n > 0 && n < kLate) {
+#pragma unroll
+          for (int x = (n - 1) * TM / 3; x < n * TM / 3; ++x) next[x] = Step::scale(rows_scale[x], b_scale);
+        }
         __builtin_amdgcn_sched_barrier(0);
         late[n % kLate] = Step::block(fa[n % TM], fb[j][n / TM], scale[n % TM]);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int k = 0; k < Step::kSteps; ++k)
 #pragma unroll
         for (int y = 0; y < TN; ++y)
 #pragma unroll
           for (int x = 0; x < TM; ++x) acc[i][j][x][y] = Step::step(fa[x], fb[j][y], acc[i][j][x][y], k);
+      __builtin_amdgcn_s_setprio(0);
     }
-    __builtin_amdgcn_s_setprio(0);
   };
 
   // The stages run through a pipeline of quarters.  The two waves of a SIMD
@@ -400,21 +404,26 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   // (With block scales every stage asks for one more, at its first quarter: six
   // quarters hold one or two of those.)
   constexpr int kAhead = 3 * (HA::kLoads + HB::kLoads) + (BLOCK ? 1 : 0);
+  // The next quarter's scales, read last, need not be there yet: the compiler
+  // reads at most two of them at a time.
+  constexpr int kScaleReads = BLOCK ? (TM + 2) / 2 : 0;
   // was_i, was_j: the quarter before; kt, next_i, next_j: the one after
   auto quarter = [&](auto read, auto fetch, int was_i, int was_j, int i, int j, int kt, int next_i, int next_j) {
+    // with block scales the wave that reads goes first: both have vector work
+    if (BLOCK) __builtin_amdgcn_s_setprio(1);
     read();
     if constexpr (BLOCK) {
       __builtin_amdgcn_sched_barrier(0);
-      add_block(was_i, was_j, kBlocks - kLate, scale);
+      settle(was_i, was_j);
 #pragma unroll
-      for (int x = 0; x < TM; ++x) was[x] = scale[x];
-      take_scales();
+      for (int x = 0; x < TM; ++x) scale[x] = next[x];
       ask_scales(kt, next_i, next_j);
     }
     fetch();
-    arrived<kAhead>();
+    if (BLOCK) __builtin_amdgcn_s_setprio(0);
+    arrived<kAhead, kScaleReads>();
     meet();
-    multiply(was_i, was_j, i, j);
+    multiply(i, j);
     meet();
   };
   if (kn > 0) {
@@ -430,7 +439,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
 #pragma unroll
       for (int n = 0; n < kLate; ++n) late[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int x = 0; x < TM; ++x) scale[x] = Step::scale(0.f, 0.f);
+      for (int x = 0; x < TM; ++x) {
+        scale[x] = Step::scale(0.f, 0.f);
+        next[x] = Step::scale(rows_scale[x], b_scale);
+      }
     }
     arrived<kAhead>();
     meet();
@@ -446,8 +458,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
       quarter([&] { read_a(1, 1); }, [&] { fetch_b(kt + 3, 1, 0); }, 0, 0, 1, 0, kt + 1, 1, 1);
       quarter([&] { read_b(0, 0); }, [&] { fetch_a(kt + 3, 1, 1); }, 1, 0, 1, 1, kt + 2, 0, 0);
     }
-#pragma unroll
-    for (int n = kBlocks - kLate; n < kBlocks; ++n) add_block(1, 1, n, scale);
+    settle(1, 1);
     if (WAVES == 8 && !wm) meet();
     // nothing may still be on its way to LDS when its bytes are used again
     arrived<0>();
