@@ -138,14 +138,17 @@ constexpr int kPiece = 4096;
 __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a, int64_t scale_groups) {
   int64_t id = block_number<256>(blockIdx.x, blockIdx.y);
   if (id < scale_groups) {
-    // scales: 64 tokens a workgroup, so that their lines are read whole
-    const int64_t token = id * 64 + threadIdx.x % 64;
-    if (token >= a.tokens) return;
+    // scales: 64 tokens a workgroup, so that their lines are read whole, and
+    // four blocks, one a wave
+    const int64_t fours = (a.blocks + 3) / 4, group = id / fours, token = group * 64 + threadIdx.x % 64;
+    const int64_t b = (id - group * fours) * 4 + threadIdx.x / 64;
+    if (token >= a.tokens || b >= a.blocks) return;
+    const float scale = a.x_scale[b * a.ldx_scale + token];
+    const int32_t *place = a.place + token * a.ld_place;
+#pragma unroll 8
     for (int j = 0; j < a.top_k; ++j) {
-      const int p = a.place[token * a.ld_place + j];
-      if ((uint32_t)p >= (uint32_t)a.pairs) continue;
-      for (int b = threadIdx.x / 64; b < a.blocks; b += 4)
-        a.y_scale[b * a.ldy_scale + p] = a.x_scale[b * a.ldx_scale + token];
+      const int p = place[j];
+      if ((uint32_t)p < (uint32_t)a.pairs) a.y_scale[b * a.ldy_scale + p] = scale;
     }
     return;
   }
@@ -164,7 +167,11 @@ __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a, int64_t s
 #pragma unroll 8
     for (int j = 0; j < a.top_k; ++j) {
       const int p = place[j];
-      if ((uint32_t)p < (uint32_t)a.pairs) __builtin_memcpy(y + p * a.ldy, &v, 16);
+      if ((uint32_t)p >= (uint32_t)a.pairs) continue;
+      if (a.aligned)
+        __builtin_nontemporal_store(v, (u32x4 *)(y + p * a.ldy));
+      else
+        __builtin_memcpy(y + p * a.ldy, &v, 16);
     }
   } else {
     for (int j = 0; j < a.top_k; ++j) {
@@ -222,21 +229,21 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 }
 
 // dy[place[t, j]] = weight[t, j] dd[t], dweight[t, j] = <dd[t], y[place[t, j]]>:
-// T threads a token, which go through its columns once for every eight choices.
-template <class E, int T>
-__global__ __launch_bounds__(256) void combine_grad_kernel(CombineArgs a) {
-  __shared__ float part[T == 64 ? 1 : kAtOnce][4];
-  constexpr int PER = 256 / T;
-  const int64_t token = block_number<256>(blockIdx.x, blockIdx.y) * PER + threadIdx.x / T;
+// T threads a token, which go through its columns once for every AT choices.
+template <class E, int T, int AT>
+__global__ __launch_bounds__(T == 64 ? 256 : T) void combine_grad_kernel(CombineArgs a) {
+  __shared__ float part[T == 64 ? 1 : AT][T / 64];
+  constexpr int PER = T == 64 ? 4 : 1;
+  const int64_t token = block_number<T == 64 ? 256 : T>(blockIdx.x, blockIdx.y) * PER + threadIdx.x / T;
   if (token >= a.tokens) return;  // whole waves, and no barrier follows where PER > 1
   const int t = threadIdx.x % T;
   const int32_t *place = a.place + token * a.ld_place;
   const float *weight = a.weight + token * a.ld_weight;
-  for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
-    float w[kAtOnce], dot[kAtOnce];
-    int p[kAtOnce];
+  for (int j0 = 0; j0 < a.top_k; j0 += AT) {
+    float w[AT], dot[AT];
+    int p[AT];
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
+    for (int j = 0; j < AT; ++j) {
       p[j] = j0 + j < a.top_k ? place[j0 + j] : -1;
       w[j] = j0 + j < a.top_k ? weight[j0 + j] : 0.f;
       dot[j] = 0.f;
@@ -244,13 +251,13 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineArgs a) {
     for (int c = t * 8; c < a.cols; c += T * 8) {
       const int left = a.cols - c;
       const bool vec = a.vec && left >= 8;
-      float g[8], v[kAtOnce][8];
+      float g[8], v[AT][8];
       get<E, 8>(a.dd, token * a.ldd + c, left, vec, g);
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
+      for (int j = 0; j < AT; ++j)
         if ((uint32_t)p[j] < (uint32_t)a.pairs) get<E, 8>(a.y, p[j] * a.ldy + c, left, vec, v[j]);
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
+      for (int j = 0; j < AT; ++j) {
         if ((uint32_t)p[j] >= (uint32_t)a.pairs) continue;
         float o[8];
 #pragma unroll
@@ -263,7 +270,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineArgs a) {
     }
     if (T != 64) __syncthreads();  // the sums of the choices before are read
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
+    for (int j = 0; j < AT; ++j) {
       const float s = wave_sum(dot[j]);
       if (T == 64) {
         if (t == 0 && j0 + j < a.top_k) a.dweight[token * a.ld_dweight + j0 + j] = s;
@@ -273,8 +280,12 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineArgs a) {
     }
     if (T != 64) {
       __syncthreads();
-      if (t < kAtOnce && j0 + t < a.top_k)
-        a.dweight[token * a.ld_dweight + j0 + t] = ((part[t][0] + part[t][1]) + part[t][2]) + part[t][3];
+      if (t < AT && j0 + t < a.top_k) {
+        float s = part[t][0];
+#pragma unroll
+        for (int i = 1; i < T / 64; ++i) s += part[t][i];
+        a.dweight[token * a.ld_dweight + j0 + t] = s;
+      }
     }
   }
 }
@@ -284,10 +295,11 @@ hipError_t combine_go(const CombineArgs &a, hipStream_t s) {
   return launch(combine_kernel<E>, grid_of<256>(a.tokens * ((a.cols + 2047) / 2048)), 256, s, a);
 }
 
-template <class E>
+template <class E, int AT>
 hipError_t combine_grad_go(const CombineArgs &a, hipStream_t s) {
-  if (a.cols <= 512) return launch(combine_grad_kernel<E, 64>, grid_of<256>((a.tokens + 3) / 4), 256, s, a);
-  return launch(combine_grad_kernel<E, 256>, grid_of<256>(a.tokens), 256, s, a);
+  if (a.cols <= 512) return launch(combine_grad_kernel<E, 64, AT>, grid_of<256>((a.tokens + 3) / 4), 256, s, a);
+  if (a.cols <= 2048) return launch(combine_grad_kernel<E, 256, AT>, grid_of<256>(a.tokens), 256, s, a);
+  return launch(combine_grad_kernel<E, 512, AT>, grid_of<512>(a.tokens), 512, s, a);
 }
 
 }  // namespace
@@ -314,7 +326,7 @@ hipError_t launch_sort(const SortArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s) {
-  const int64_t scale_groups = a.x_scale ? (a.tokens + 63) / 64 : 0;
+  const int64_t scale_groups = a.x_scale ? (a.tokens + 63) / 64 * ((a.blocks + 3) / 4) : 0;
   return launch(dispatch_kernel, grid_of<256>(scale_groups + a.tokens * ((a.bytes + kPiece - 1) / kPiece)), 256, s, a,
                 scale_groups);
 }
@@ -326,9 +338,9 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_combine_grad(const CombineArgs &a, hipStream_t s) {
-  if (a.dtype == HF_BF16) return combine_grad_go<BF16>(a, s);
-  if (a.dtype == HF_F16) return combine_grad_go<F16>(a, s);
-  return combine_grad_go<F32>(a, s);
+  if (a.dtype == HF_BF16) return a.top_k <= 4 ? combine_grad_go<BF16, 4>(a, s) : combine_grad_go<BF16, 8>(a, s);
+  if (a.dtype == HF_F16) return a.top_k <= 4 ? combine_grad_go<F16, 4>(a, s) : combine_grad_go<F16, 8>(a, s);
+  return a.top_k <= 4 ? combine_grad_go<F32, 4>(a, s) : combine_grad_go<F32, 8>(a, s);
 }
 
 }  // namespace hf

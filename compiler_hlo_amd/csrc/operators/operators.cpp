@@ -919,6 +919,7 @@ hipError_t run_dispatch(const Call &c) {
   }
   a.tokens = op.d.m;
   a.bytes = op.d.n * elem;
+  a.aligned = aligned16(op.buf[y]);
   a.top_k = (int)op.top_k;
   a.pairs = (int)(op.d.m * op.top_k);
   return launch_dispatch(a, c.stream);

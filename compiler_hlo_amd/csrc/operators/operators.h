@@ -74,6 +74,7 @@ struct DispatchArgs {
   int64_t ld_place, ldx_scale, ldy_scale;
   int64_t tokens, bytes;         // of a row
   int32_t top_k, pairs, blocks;
+  bool aligned;                  // y's rows start on 16 bytes
 };
 hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s);
 

@@ -684,7 +684,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
   const int c0 = (int)(id - group * wide) * 2048, c = c0 + threadIdx.x * 8, left = a.cols - c;
   const bool vec = a.vec && left >= 8;
   const int rows = a.rows - row0 < R ? (int)(a.rows - row0) : R;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = R < 4 ? R : 4;
 #pragma unroll
   for (int r0 = 0; r0 < R; r0 += kAhead) {
     if (r0 >= rows) break;
@@ -701,7 +701,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[r][i]) & 0x7fffffffu);
       const float scale = __uint_as_float(sixteen_max(top)) / 448.f;
-      if (threadIdx.x % 16 == 0) scales[r0 + r][threadIdx.x / 16] = scale;
+      if (R > 1 && threadIdx.x % 16 == 0) scales[r0 + r][threadIdx.x / 16] = scale;
+      if (R == 1 && threadIdx.x % 16 == 0 && left > 0) a.scale[(c / 128) * a.ld_scale + row0] = scale;
       const Quotient q(scale);
       float o[8];
 #pragma unroll
@@ -720,17 +721,19 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
       }
     }
   }
+  if (R == 1) return;
   __syncthreads();
   const int b = threadIdx.x / R, r = threadIdx.x % R;
   if (b < 16 && r < rows && c0 / 128 + b < (a.cols + 127) / 128) a.scale[(c0 / 128 + b) * a.ld_scale + row0 + r] = scales[r][b];
 }
 
 // 16 rows a workgroup where that still makes four workgroups a compute unit,
-// so that a block's scales go out as 64 bytes; else 4.
+// so that a block's scales go out as 64 bytes; else 4, and of few rows one.
 template <class E>
 hipError_t quantize_go(const QuantizeArgs &a, hipStream_t s) {
   const int64_t wide = (a.cols + 2047) / 2048;
   if (wide * (a.rows / 16) >= 1024) return launch(quantize_kernel<E, 16>, grid_of<256>(wide * ((a.rows + 15) / 16)), 256, s, a);
+  if (a.rows <= 16) return launch(quantize_kernel<E, 1>, grid_of<256>(wide * a.rows), 256, s, a);
   return launch(quantize_kernel<E, 4>, grid_of<256>(wide * ((a.rows + 3) / 4)), 256, s, a);
 }
 
