@@ -162,8 +162,9 @@ double expert_threads(const hf_operator &op) {
   const Product &p = op.p1, &q = op.p2;
   double n = 0;
   const int64_t rows = p.tile == 0 ? 256 : p.tile == 1 ? 128 : 64, cols = p.tile == 0 ? 256 : 128;
-  if (p.on) n += (double)expert_tiles(p.m, p.experts, rows, 1) * (double)cdiv(p.n, p.gated ? cols / 2 : cols);
-  if (q.on) n += (double)q.experts * (double)cdiv(q.m, rows) * (double)cdiv(q.n, cols);
+  if (p.on) n += (double)expert_tiles(p.m, p.experts, rows, 1) * (double)cdiv(p.n, p.gated ? cols / 2 : cols) + 128;
+  // dealt out in whole turns of eight chunks, a 64th of the tiles each at most
+  if (q.on) n += 1.125 * (double)q.experts * (double)cdiv(q.m, rows) * (double)cdiv(q.n, cols) + 8;
   return n * (p.tile == 1 ? 256 : 512);
 }
 

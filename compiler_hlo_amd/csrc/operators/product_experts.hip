@@ -5,16 +5,38 @@
 namespace hf {
 namespace {
 
-// Tiles of 2 HM rows of one expert.  How many there are is in the offsets on
-// the GPU: the grid holds as many as any offsets can ask for, and a workgroup
-// without a tile ends at once.
-template <class Step, int HM, int HN>
-__global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_kernel(ProductArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[Shape<HM, HN>::lds(Step::kBlock)];
-  const int width = a.e.gated ? HN : 2 * HN;
+// A tile of 256 x 256 of an expert, or, where it has no more than 128 rows or
+// is cut, a half or two of them of 128 x 256, which take about 0.6 of its time.
+template <class Step, bool ACOL, bool BCOL>
+__device__ __forceinline__ void large_tile(const ProductArgs &a, const ExpertTile &t, int tiles_n, char *lds) {
+  int tm, tn;
+  tile_at(t.local, (t.rows + 255) / 256, tiles_n, tm, tn);
+  const int from = tm * 256 + (t.half > 0 ? 128 : 0), left = t.rows - from;
+  if (left <= 0) return;
+  if (t.half >= 0 || left <= 128)
+    product_tile<Step, ACOL, BCOL, 64, 128, true>(part_of(a, t.expert, t.row + from, min(left, 128)), tn, lds);
+  else
+    product_tile<Step, ACOL, BCOL, 128, 128, true>(part_of(a, t.expert, t.row, t.rows), t.local, lds);
+}
+
+// Tiles of 256 or of 128 rows of one expert.  How many there are is in the
+// offsets on the GPU: the grid holds as many as any offsets can ask for, and a
+// workgroup without a tile ends at once.
+template <class Step>
+__global__ __launch_bounds__(512, 2) void experts_large_kernel(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<128, 128>::lds(Step::kBlock)];
+  const int width = a.e.gated ? 128 : 256, tiles_n = (a.n + width - 1) / width;
   ExpertTile t;
-  if (!expert_tile(a.offsets, a.experts, a.m, 2 * HM, (a.n + width - 1) / width, blockIdx.x, t)) return;
-  product_tile<Step, false, false, HM, HN, true>(part_of(a, t.expert, t.row, t.rows), t.local, lds);
+  if (expert_tile<true>(a.offsets, a.experts, a.m, 256, tiles_n, blockIdx.x, t)) large_tile<Step, false, false>(a, t, tiles_n, lds);
+}
+
+template <class Step>
+__global__ __launch_bounds__(256, 2) void experts_small_kernel(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<64, 64>::lds(Step::kBlock)];
+  const int width = a.e.gated ? 64 : 128;
+  ExpertTile t;
+  if (!expert_tile<false>(a.offsets, a.experts, a.m, 128, (a.n + width - 1) / width, blockIdx.x, t)) return;
+  product_tile<Step, false, false, 64, 64, true>(part_of(a, t.expert, t.row, t.rows), t.local, lds);
 }
 
 // Strips for up to 64 rows of an expert, bound by reading the weights.  An
@@ -26,7 +48,7 @@ __global__ __launch_bounds__(512, 2) void experts_strip_kernel(ProductArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[Strip<Step>::kLds];
   const int width = a.e.gated ? 64 : 128;
   ExpertTile t;
-  if (!expert_tile(a.offsets, a.experts, a.m, 64, (a.n + width - 1) / width, blockIdx.x, t)) return;
+  if (!expert_tile<false>(a.offsets, a.experts, a.m, 64, (a.n + width - 1) / width, blockIdx.x, t)) return;
   const int units = (t.rows + 63) / 64, strip = t.local / units, from = (t.local - strip * units) * 64;
   strip_tile<Step>(part_of(a, t.expert, t.row + from, min(64, t.rows - from)), strip, 0, blockIdx.x / 8 * 7u, lds);
 }
@@ -52,8 +74,11 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_gradient_ker
   const int tiles_n = (max(da.n, db.n) + 2 * HN - 1) / (2 * HN);  // of one that may be empty
   if ((int)blockIdx.x < first) {
     ExpertTile t;
-    if (!expert_tile(da.offsets, da.experts, da.m, 2 * HM, tiles_n, blockIdx.x, t)) return;
-    product_tile<Step, false, true, HM, HN, true>(part_of(da, t.expert, t.row, t.rows), t.local, lds);
+    if (!expert_tile<false>(da.offsets, da.experts, da.m, 2 * HM, tiles_n, blockIdx.x, t)) return;
+    if constexpr (HM == 128)
+      large_tile<Step, false, true>(da, t, tiles_n, lds);
+    else
+      product_tile<Step, false, true, HM, HN, true>(part_of(da, t.expert, t.row, t.rows), t.local, lds);
     return;
   }
   const int tiles = (db.m + 2 * HM - 1) / (2 * HM) * tiles_n, all = tiles * db.experts;
@@ -79,8 +104,12 @@ hipError_t go(const ProductArgs &a, hipStream_t s) {
     return dim3((unsigned)expert_tiles(a.m, a.experts, rows, (a.n + width - 1) / width));
   };
   if (a.tile == 2) return launch(experts_strip_kernel<Step>, groups(64, 128), 512, s, a);
-  if (a.tile == 1) return launch(experts_kernel<Step, 64, 64>, groups(128, 128), 256, s, a);
-  if constexpr (!Step::kWide) return launch(experts_kernel<Step, 128, 128>, groups(256, 256), 512, s, a);
+  if (a.tile == 1) return launch(experts_small_kernel<Step>, groups(128, 128), 256, s, a);
+  if constexpr (!Step::kWide) {
+    dim3 grid = groups(256, 256);
+    grid.x += 128;  // the halves of as many tiles
+    return launch(experts_large_kernel<Step>, grid, 512, s, a);
+  }
   return hipErrorInvalidValue;  // never planned with kWide
 }
 

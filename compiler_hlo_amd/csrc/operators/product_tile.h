@@ -649,9 +649,19 @@ __device__ __forceinline__ void strip_tile(const ProductArgs &a, int strip, int 
 // about 1 us, against 10 us and more that a tile takes, and no launch or wait
 // of a kernel that would write a list.  As in product_tile, each XCD takes a
 // contiguous run of tiles.
+//
+// CUT: the last tiles, which would leave more than half of the 256 compute
+// units without one, are cut into an upper and a lower half, a workgroup's
+// each.
 struct ExpertTile {
   int expert, row, rows, local;
+  int half;  // 0 or 1: that half of the tile's rows, -1: all
 };
+__device__ __forceinline__ int xcd_run(int block, int count) {
+  const int xcd = block % 8, q = count / 8, r = count % 8;
+  return xcd * q + min(xcd, r) + block / 8;
+}
+template <bool CUT>
 __device__ __forceinline__ bool expert_tile(const int32_t *offsets, int experts, int m, int size, int per, int block,
                                             ExpertTile &t) {
   const int l = threadIdx.x % 64;
@@ -670,9 +680,17 @@ __device__ __forceinline__ bool expert_tile(const int32_t *offsets, int experts,
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) all += __shfl_xor(all, d);
   const int total = __builtin_amdgcn_readfirstlane((int)min(all, (int64_t)0x7fffffff));
-  const int xcd = block % 8, j = block / 8, q = total / 8, r = total % 8;
-  if (j >= q + (xcd < r ? 1 : 0)) return false;
-  int id = xcd * q + min(xcd, r) + j;
+  const int cut = CUT && total % 256 <= 128 ? total % 256 : 0, whole = total - cut;
+  if (block >= whole + 2 * cut) return false;
+  int id;
+  t.half = -1;
+  if (block < whole) {
+    id = xcd_run(block, whole);
+  } else {
+    id = xcd_run(block - whole, 2 * cut);
+    t.half = id % 2;
+    id = whole + id / 2;
+  }
   for (int first = 0; first < experts; first += 64) {
     const int n = tiles(first + l, lo, hi);
     int sum = n;

@@ -481,6 +481,31 @@ def test_experts_product_tiles():
     assert {t for _, t in seen} == {64, 128, 256}
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "blocks"])
+@pytest.mark.parametrize("counts", [[1300, 90, 513, 700],       # 208 large tiles: whole, ragged ends as halves
+                                    [2600, 90, 0, 513, 700],    # 288: 256 whole ones, the last 32 cut into halves
+                                    [257, 255, 256, 128]])      # few: all cut
+def test_experts_large_tiles(dtype, counts):
+    n, k, behind = 4096 if len(counts) > 4 or counts[0] > 1000 else 700, 136, 5
+    for parts in (1, 2):
+        cols = n // parts
+        g = gen(sum(counts) + parts)
+        m = sum(counts) + behind
+        ops, z, mag = experts_operands(g, dtype, m, cols, k, len(counts), parts, counts)
+        make = H.Matmul if parts == 1 else H.GatedFeedForward
+        op = make(m, cols, k, "f8e4m3" if dtype == "blocks" else dtype, out_dtype="bf16", activation="relu", save=True,
+                  experts=len(counts), scales="blocks" if dtype == "blocks" else None)
+        assert op.plan()["tile_rows"] == 256 or len(counts) > 4 or counts[0] < 1000
+        say("experts large", dtype, counts, cols, k, parts, op.plan())
+        out = [b.empty("cuda") for b in op.results]
+        for t in out:
+            t.fill_(5.0)
+        d, zs = op(*ops, out=out)
+        err = product_error(mag, k)
+        R.close(zs[:z.shape[0]], z, err, torch.bfloat16)
+        assert (d[z.shape[0]:] == 5.0).all() and (zs[z.shape[0]:] == 5.0).all()
+
+
 def grads_want(dz, a, b, ends, experts):
     """(da, db) and the magnitudes of their sums, in 64 bits."""
     wide, k = dz.shape[1], a.shape[1]
