@@ -58,12 +58,30 @@ __global__ __launch_bounds__(512, 2) void experts_strip_kernel(ProductArgs a) {
 // chunks of up to four tile rows, which share their operands in an L2, and the
 // first XCD moves on by one with every eight chunks.  (16 experts of 1024 rows
 // on average, some with three times as many as others, 16384 x 4096 x 1408 bf16:
-// 322 us for db in contiguous runs.)
+// 501 us with contiguous runs.)
 __device__ __forceinline__ int dealt(int block, int chunk) {
   const int xcd = block % 8, j = block / 8, turn = j / chunk;
   return (turn * 8 + (xcd + turn) % 8) * chunk + j % chunk;
 }
-__host__ __device__ __forceinline__ int chunk_of(int all, int tiles_n) { return max(1, min(4 * tiles_n, all / 64)); }
+__host__ __device__ __forceinline__ int chunk_of(int all, int tiles_n) { return max(1, min(4 * tiles_n, all / 128)); }
+
+// The expert with the `place`-th most rows (of equal ones the lower first), so
+// that the longest tiles begin first; of more than 64 experts the place itself.
+__device__ __forceinline__ int by_rows(const int32_t *offsets, int experts, int m, int place) {
+  if (experts > 64) return place;
+  const int l = threadIdx.x % 64;
+  int rows = -1;
+  if (l < experts) {
+    const int lo = min(max(offsets[l], 0), m);
+    rows = min(max(offsets[l + 1], lo), m) - lo;
+  }
+  int before = 0;
+  for (int e = 0; e < experts; ++e) {
+    const int r = __builtin_amdgcn_readlane(rows, e);
+    before += r > rows || (r == rows && e < l) ? 1 : 0;
+  }
+  return __builtin_ctzll(__ballot(l < experts && before == place));
+}
 
 // The gradient: da as the products above, with b's rows as the contraction,
 // and db[e] = dz^T a over the expert's rows (zeros where it has none), in one
@@ -84,7 +102,7 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_gradient_ker
   const int tiles = (db.m + 2 * HM - 1) / (2 * HM) * tiles_n, all = tiles * db.experts;
   const int id = dealt(blockIdx.x - first, chunk_of(all, tiles_n));
   if (id >= all) return;
-  const int expert = id / tiles;
+  const int expert = by_rows(db.offsets, db.experts, db.k, id / tiles);
   const int row = min(max(db.offsets[expert], 0), db.k);
   const int rows = min(max(db.offsets[expert + 1], row), db.k) - row;
   ProductArgs p = db;
@@ -94,7 +112,7 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_gradient_ker
   p.b_bytes = rows > 0 ? (rows - 1) * db.ldb + db.b_bytes : 0;
   p.k = rows;
   p.e.d = (char *)db.e.d + expert * (int64_t)db.m * db.e.ldd * 2;
-  product_tile<Step, true, true, HM, HN, true>(p, id - expert * tiles, lds);
+  product_tile<Step, true, true, HM, HN, true>(p, id % tiles, lds);
 }
 
 template <class Step>
