@@ -291,13 +291,33 @@ void place_partials(hf_operator &op, Product &p) {
 }
 
 // Products by expert.  How the rows are shared out is not known here, so the
-// tile goes by the rows that an expert has if all have as many.
+// kernel goes by the rows that an expert has if all have as many (measured with
+// the most liked of 8 to 64 experts at two to three times that):
+// - up to 24, strips (16 experts of 16 rows, gated 2048 x 4096 e4m3 with block
+//   scales 57 us, small tiles 68; 32 of 32 rows, 4096 x 1408 bf16 91 and 79);
+// - large tiles from 160 on (8 of 256, gated 4096 x 4096 bf16 177 us, small 203;
+//   32 of 96, gated 1408 x 4096 207 and 185), with block scales from 640 on, as
+//   two small ones a compute unit hide the scales' additions (8 of 512, gated
+//   4096 x 4096 235 us, small 221; of 1024 367 and 378), where they make 128 or
+//   more (8 of 256, 512 x 512 bf16 14.5 us, small 11.9);
+// - small tiles between.
 void choose_experts(const hf_operator &op, Product &p, bool wide) {
   p.on = p.m > 0 && p.n > 0;
   p.experts = op.experts;
   const int64_t rows = p.m / std::max<int64_t>(1, std::min(op.experts, p.m));
-  p.tile = rows <= 64 ? 2 : wide || rows <= 192 ? 1 : 0;
+  const int64_t from = op.d.flags & HF_OPERATOR_BLOCK_SCALES ? 640 : 160;
+  const bool large = !wide && rows >= from && p.m / 256 * cdiv(p.n, p.gated ? 128 : 256) >= 128;
+  p.tile = rows <= 24 ? 2 : large ? 0 : 1;
   p.per_split = (int)std::max<int64_t>(1, cdiv(p.k, 128 / op.buf[0].elem()));
+}
+
+// A gradient by expert: large tiles where db has 128 or more (16 experts of 256
+// rows, 4096 x 1408 bf16 170 us, small 184; 8 of 64, 4096 x 4096 164 and 182).
+void choose_experts_gradient(const hf_operator &op, Product &p, Product &q) {
+  p.on = p.m > 0 && p.n > 0;
+  q.on = q.m > 0 && q.n > 0;
+  p.experts = q.experts = op.experts;
+  p.tile = q.tile = op.experts * cdiv(q.m, 256) * cdiv(q.n, 256) >= 128 ? 0 : 1;
 }
 
 void plan_norm(hf_operator &op) {
@@ -468,10 +488,7 @@ void plan_product_grad(hf_operator &op) {
   q.a.cols = up(wide, 8);
   q.b = a;
   if (op.experts) {
-    choose_experts(op, p, false);
-    q.on = q.m > 0 && q.n > 0;
-    q.experts = op.experts;
-    p.tile = q.tile = std::min(p.tile, 1);
+    choose_experts_gradient(op, p, q);
     return;
   }
   choose_gradient(p, q);

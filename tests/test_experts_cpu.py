@@ -212,12 +212,24 @@ def test_workspaces():
     assert H.Matmul(64, 16, 1023, experts=8, mode="plan").workspace_bytes >= 2 * 1024 * (64 + 128)
 
 
-@pytest.mark.parametrize("m, experts, want", [
-    (64, 64, (64, 128)),     # a row an expert: strips
-    (4096, 64, (64, 128)),   # 64 rows an expert
-    (8192, 64, (128, 128)),
-    (16384, 64, (256, 256)),
+@pytest.mark.parametrize("m, n, experts, dtype, want", [
+    (64, 2048, 64, "bf16", 64),        # a row an expert: strips
+    (24 * 64, 2048, 64, "bf16", 64),
+    (25 * 64, 2048, 64, "bf16", 128),
+    (159 * 16, 4096, 16, "bf16", 128),
+    (160 * 16, 4096, 16, "bf16", 256),
+    (2048, 512, 8, "bf16", 128),       # too few large tiles
+    (160 * 16, 4096, 16, "blocks", 128),
+    (640 * 16, 4096, 16, "blocks", 256),
+    (640 * 16, 4096, 16, "f32", 128),  # e4m3 through f16
+    (7, 4096, 64, "bf16", 64),
 ])
-def test_tile_choices_by_expert(m, experts, want):
-    p = H.Matmul(m, 2048, 2048, experts=experts, mode="plan").plan()
-    assert (p["tile_rows"], p["tile_cols"]) == want and p["splits"] == 1
+def test_tile_choices_by_expert(m, n, experts, dtype, want):
+    kw = {"bf16": {}, "blocks": dict(dtype="f8e4m3", scales="blocks"), "f32": dict(dtype="f8e4m3", out_dtype="f32")}[dtype]
+    p = H.Matmul(m, n, 2048, experts=experts, mode="plan", **kw).plan()
+    assert p["tile_rows"] == want and p["tile_cols"] == max(want, 128) and p["splits"] == 1
+
+
+@pytest.mark.parametrize("n, k, experts, want", [(4096, 1408, 16, 256), (512, 512, 8, 128), (1024, 1024, 8, 256)])
+def test_tile_choices_of_gradients_by_expert(n, k, experts, want):
+    assert H.MatmulGrad(100, n, k, experts=experts, mode="plan").plan()["tile_rows"] == want

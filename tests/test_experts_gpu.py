@@ -462,12 +462,11 @@ def test_experts_product(dtype, counts, n, k):
 
 
 def test_experts_product_tiles():
-    """Every tile that a product by expert takes: strips, small and large tiles,
-    each with more than one tile of rows and of columns."""
+    """Strips and small tiles, each with more than one tile of rows and of
+    columns."""
     seen = set()
-    for dtype, counts, n, k in (("bf16", [20, 90, 0, 7], 300, 256), ("f16", [150, 0, 400, 20], 600, 328),
-                                ("bf16", [700, 90, 513, 0], 600, 520), ("f8e4m3", [700, 90, 513, 0], 600, 520),
-                                ("blocks", [700, 90, 513, 0], 600, 520), ("s8", [700, 90, 513, 0], 600, 520)):
+    for dtype, counts, n, k in (("bf16", [20, 90, 0, 0, 0, 7], 300, 256), ("f16", [150, 0, 400, 20], 600, 328),
+                                ("blocks", [33, 90, 0, 0, 0, 0, 0], 600, 520), ("s8", [700, 90, 513, 0], 600, 520)):
         for parts in (1, 2):
             g = gen(n + parts)
             ops, z, mag = experts_operands(g, dtype, sum(counts), n, k, len(counts), parts, counts)
@@ -475,35 +474,78 @@ def test_experts_product_tiles():
             make = H.Matmul if parts == 1 else H.GatedFeedForward
             op = make(sum(counts), n, k, kind, out_dtype=out, activation="relu", save=True, experts=len(counts),
                       scales="blocks" if dtype == "blocks" else None)
-            seen.add((dtype, op.plan()["tile_rows"]))
+            seen.add(op.plan()["tile_rows"])
             say("experts tiles", dtype, counts, n, k, parts, op.plan())
             R.close(op(*ops)[1], z, product_error(mag, k), T[out])
-    assert {t for _, t in seen} == {64, 128, 256}
+    assert seen == {64, 128}
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "blocks"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "s8", "f8e4m3", "blocks"])
 @pytest.mark.parametrize("counts", [[1300, 90, 513, 700],       # 208 large tiles: whole, ragged ends as halves
                                     [2600, 90, 0, 513, 700],    # 288: 256 whole ones, the last 32 cut into halves
-                                    [257, 255, 256, 128]])      # few: all cut
+                                    [1024, 900, 300]])          # 160 of 256 rows: whole, ragged
 def test_experts_large_tiles(dtype, counts):
-    n, k, behind = 4096 if len(counts) > 4 or counts[0] > 1000 else 700, 136, 5
+    k, behind = 136, 5
     for parts in (1, 2):
-        cols = n // parts
+        n = 4096 // parts - 8
         g = gen(sum(counts) + parts)
         m = sum(counts) + behind
-        ops, z, mag = experts_operands(g, dtype, m, cols, k, len(counts), parts, counts)
+        ops, z, mag = experts_operands(g, dtype, m, n, k, len(counts), parts, counts)
         make = H.Matmul if parts == 1 else H.GatedFeedForward
-        op = make(m, cols, k, "f8e4m3" if dtype == "blocks" else dtype, out_dtype="bf16", activation="relu", save=True,
+        half = "f16" if dtype == "f16" else "bf16"
+        op = make(m, n, k, "f8e4m3" if dtype == "blocks" else dtype, out_dtype=half, activation="relu", save=True,
                   experts=len(counts), scales="blocks" if dtype == "blocks" else None)
-        assert op.plan()["tile_rows"] == 256 or len(counts) > 4 or counts[0] < 1000
-        say("experts large", dtype, counts, cols, k, parts, op.plan())
+        assert op.plan()["tile_rows"] == 256
+        say("experts large", dtype, counts, n, k, parts, op.plan())
         out = [b.empty("cuda") for b in op.results]
         for t in out:
             t.fill_(5.0)
         d, zs = op(*ops, out=out)
         err = product_error(mag, k)
-        R.close(zs[:z.shape[0]], z, err, torch.bfloat16)
+        R.close(zs[:z.shape[0]], z, err, T[half])
         assert (d[z.shape[0]:] == 5.0).all() and (zs[z.shape[0]:] == 5.0).all()
+
+
+def test_experts_large_tiles_all_cut():
+    """128 large tiles, every one cut into two halves."""
+    counts, n, k = [1024, 768, 256], 4096, 72
+    g = gen(128)
+    ops, z, mag = experts_operands(g, "f16", sum(counts), n, k, 3, 1, counts)
+    op = H.Matmul(sum(counts), n, k, "f16", experts=3)
+    assert op.plan()["tile_rows"] == 256
+    R.close(op(*ops), z, product_error(mag, k), torch.float16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts", [[500, 0, 257, 130], [1, 700, 64, 0, 128]])
+def test_experts_gradient_large_tiles(dtype, counts):
+    experts, m, n, k = len(counts), sum(counts) + 3, 2048, 1032
+    offsets, live = offsets_of(counts), sum(counts)
+    for parts in (1, 2):
+        cols = n // parts
+        g = gen(m + parts)
+        dd, a = normal(g, (m, cols), dtype, 0.1), normal(g, (m, k), dtype)
+        b = normal(g, (experts * n, k), dtype, k ** -0.5)
+        z = normal(g, (m, n), dtype)
+        make = H.MatmulGrad if parts == 1 else H.GatedFeedForwardGrad
+        op = make(m, cols, k, dtype, experts=experts, **({} if parts == 1 else dict(activation="relu")))
+        assert op.plan()["tile_rows"] == 256
+        say("experts gradient large", dtype, counts, parts, op.plan())
+        out = [x.empty("cuda") for x in op.results]
+        for t in out:
+            t.fill_(5.0)
+        da, db = op(*([dd, a, b] + [z] * (parts - 1) + [offsets.cuda()]), out=out)
+        dz, rounded = R.f64(dd)[:live], 0.0
+        if parts == 2:
+            gate, u = R.f64(z)[:live, :cols], R.f64(z)[:live, cols:]
+            f, df = R.act("relu", gate)
+            dz = torch.cat([dz * u * df, dz * f], 1)
+            rounded = dz.abs() * (R.HALF[T[dtype]] * (1 + 2.0 ** -7) + 4 * 2.0 ** -24) + R.TINY[T[dtype]]
+        want = grads_want(dz, R.f64(a)[:live], R.f64(b), offsets.tolist(), experts)
+        off = grads_want(dz * 0 + rounded, R.f64(a)[:live].abs(), R.f64(b).abs(), offsets.tolist(), experts)
+        R.close(da[:live], want[0], R.sum_error(want[2], n) + 1.1 * off[0], T[dtype])
+        R.close(db, want[1], R.sum_error(want[3], max(counts)) + 1.1 * off[1], T[dtype])
+        assert (da[live:] == 5.0).all()
 
 
 def grads_want(dz, a, b, ends, experts):
