@@ -349,7 +349,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   // turn.  (A matrix instruction takes 32 cycles, 34 with two vector
   // instructions behind it and 40 with four, so a quarter's additions are
   // divided between the two sections.)
-  constexpr int kBlocks = TM * TN, kLate = 4;
+  constexpr int kBlocks = TM * TN, kLate = 3;
   f32x4 late[BLOCK ? kLate : 1];
   auto add_block = [&](int i, int j, int n) {
     if constexpr (BLOCK) {
@@ -368,7 +368,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
         if (n >= kLate) add_block(i, j, n - kLate);
         if (n > 0 && n < kLate) {
 #pragma unroll
-          for (int x = (n - 1) * TM / 3; x < n * TM / 3; ++x) next[x] = Step::scale(rows_scale[x], b_scale);
+          for (int x = (n - 1) * TM / (kLate - 1); x < n * TM / (kLate - 1); ++x) next[x] = Step::scale(rows_scale[x], b_scale);
         }
         __builtin_amdgcn_sched_barrier(0);
         late[n % kLate] = Step::block(fa[n % TM], fb[j][n / TM], scale[n % TM]);

@@ -405,6 +405,7 @@ COUNTS = {
     "all to one": ([0, 0, 333, 0], 3),
     "none": ([0, 0, 0], 17),
     "many": ([(i * 7) % 5 for i in range(200)], 9),
+    "a token": ([1 if i in (5, 62) else 0 for i in range(64)], 0),
 }
 
 
