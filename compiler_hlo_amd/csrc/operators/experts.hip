@@ -134,8 +134,10 @@ __global__ __launch_bounds__(kSortWaves * 64) void sort_kernel(SortArgs a) {
 // y[place[t, j]] = x[t], in bytes: a workgroup takes 4 KB of a token's row,
 // reads them once and stores them top_k times, in unaligned accesses of 16
 // bytes if need be.  Bound by the stores.
+// Shorter rows share a workgroup, 2^shift threads each.
 constexpr int kPiece = 4096;
-__global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a, int64_t scale_groups) {
+template <bool SHORT>
+__global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a, int64_t scale_groups, int shift) {
   int64_t id = block_number<256>(blockIdx.x, blockIdx.y);
   if (id < scale_groups) {
     // scales: 64 tokens a workgroup, so that their lines are read whole, and
@@ -153,9 +155,10 @@ __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a, int64_t s
     return;
   }
   id -= scale_groups;
-  const int64_t pieces = (a.bytes + kPiece - 1) / kPiece, token = id / pieces;
+  const int64_t pieces = SHORT ? 1 : (a.bytes + kPiece - 1) / kPiece;
+  const int64_t token = SHORT ? (id << (8 - shift)) + (threadIdx.x >> shift) : id / pieces;
   if (token >= a.tokens) return;
-  const int64_t c = (id - token * pieces) * kPiece + threadIdx.x * 16;
+  const int64_t c = SHORT ? (threadIdx.x & ((1 << shift) - 1)) * 16 : (id - token * pieces) * kPiece + threadIdx.x * 16;
   if (c >= a.bytes) return;
   const int left = a.bytes - c < 16 ? (int)(a.bytes - c) : 16;
   const char *x = (const char *)a.x + token * a.ldx + c;
@@ -182,18 +185,28 @@ __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs a, int64_t s
   }
 }
 
+// Threads of a short row: the least power of two that is enough.
+int threads_shift(int64_t threads) {
+  int s = 0;
+  while ((int64_t(1) << s) < threads) ++s;
+  return s;
+}
+
 // ---- combine ---------------------------------------------------------------
 // d[t] = sum_j weight[t, j] y[place[t, j]] + residual[t]: a thread has eight
 // columns of a token and asks for up to eight rows before it adds the first.
+// Short rows share a workgroup as in the dispatch.
 // Sums are in f32, in the order of j, rounded once.
 constexpr int kAtOnce = 8;
 
-template <class E>
-__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
-  const int pieces = (a.cols + 2047) / 2048;
-  const int64_t id = block_number<256>(blockIdx.x, blockIdx.y), token = id / pieces;
+template <class E, bool SHORT>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int shift) {
+  const int pieces = SHORT ? 1 : (a.cols + 2047) / 2048;
+  const int64_t id = block_number<256>(blockIdx.x, blockIdx.y);
+  const int64_t token = SHORT ? (id << (8 - shift)) + (threadIdx.x >> shift) : id / pieces;
   if (token >= a.tokens) return;
-  const int c = (int)(id - token * pieces) * 2048 + threadIdx.x * 8, left = a.cols - c;
+  const int c = SHORT ? (threadIdx.x & ((1 << shift) - 1)) * 8 : (int)(id - token * pieces) * 2048 + threadIdx.x * 8;
+  const int left = a.cols - c;
   if (left <= 0) return;
   const bool vec = a.vec && left >= 8;
   const int32_t *place = a.place + token * a.ld_place;
@@ -292,7 +305,11 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void combine_grad_kernel(Combine
 
 template <class E>
 hipError_t combine_go(const CombineArgs &a, hipStream_t s) {
-  return launch(combine_kernel<E>, grid_of<256>(a.tokens * ((a.cols + 2047) / 2048)), 256, s, a);
+  if (a.cols <= 1024) {
+    const int shift = threads_shift((a.cols + 7) / 8), per = 256 >> shift;
+    return launch(combine_kernel<E, true>, grid_of<256>((a.tokens + per - 1) / per), 256, s, a, shift);
+  }
+  return launch(combine_kernel<E, false>, grid_of<256>(a.tokens * ((a.cols + 2047) / 2048)), 256, s, a, 8);
 }
 
 template <class E, int AT>
@@ -327,8 +344,13 @@ hipError_t launch_sort(const SortArgs &a, hipStream_t s) {
 
 hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s) {
   const int64_t scale_groups = a.x_scale ? (a.tokens + 63) / 64 * ((a.blocks + 3) / 4) : 0;
-  return launch(dispatch_kernel, grid_of<256>(scale_groups + a.tokens * ((a.bytes + kPiece - 1) / kPiece)), 256, s, a,
-                scale_groups);
+  if (a.bytes <= kPiece / 2) {
+    const int shift = threads_shift((a.bytes + 15) / 16), per = 256 >> shift;
+    return launch(dispatch_kernel<true>, grid_of<256>(scale_groups + (a.tokens + per - 1) / per), 256, s, a, scale_groups,
+                  shift);
+  }
+  return launch(dispatch_kernel<false>, grid_of<256>(scale_groups + a.tokens * ((a.bytes + kPiece - 1) / kPiece)), 256, s,
+                a, scale_groups, 8);
 }
 
 hipError_t launch_combine(const CombineArgs &a, hipStream_t s) {

@@ -59,7 +59,8 @@ def chosen(g, tokens, top_k, experts, shard):
 
 
 LAYOUTS = [(1, 8, 64, 4096), (3, 2, 5, 7), (24, 8, 128, 1000), (129, 1, 3, 64), (300, 5, 16, 2056), (65, 11, 40, 4104),
-           (2, 20, 30, 513), (500, 3, 7, 16391), (33, 2, 4, 1)]
+           (2, 20, 30, 513), (500, 3, 7, 16391), (33, 2, 4, 1), (1000, 9, 20, 130),
+           (700, 2, 8, 1024), (515, 4, 9, 65)]
 
 
 @pytest.mark.parametrize("tokens, top_k, experts, cols", LAYOUTS)
@@ -236,7 +237,7 @@ def check_quantize(x, y, scale):
 
 
 @pytest.mark.parametrize("rows, cols", [(1, 11264), (1, 1), (5, 127), (4, 128), (17, 129), (33, 2048), (9, 2049), (100, 1000),
-                                        (4100, 1111), (2500, 16384), (16, 20)])
+                                        (4100, 1111), (2500, 16384), (16, 20), (70000, 40), (9000, 512), (3000, 300), (333, 1024)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_quantize(dtype, rows, cols):
     for stride in (None, cols + 1, cols + 16):
