@@ -14,9 +14,11 @@ namespace {
 // find each other by a ballot for each bit of the expert's number, and their
 // rank is the number of them in lower lanes.  No order depends on time.
 //
-// One workgroup does it all for up to 8192 pairs (192 pairs of 128 experts:
-// a launch and a few dependent steps); beyond that each chunk of pairs has a
-// workgroup, and a first launch counts by chunk.
+// One workgroup does it all for up to 8192 pairs (192 pairs of 128 experts
+// 3.4 us, a launch and a few dependent steps); beyond that each chunk of pairs
+// has a workgroup, and a first launch counts by chunk (65528 pairs of 64
+// experts 4.6 + 6.3 us; every workgroup of the second adds up the counts of all
+// chunks by itself, which a third launch would cost more than).
 constexpr int kSortWaves = 16, kSortMost = 1024;  // waves; experts
 
 __device__ __forceinline__ int expert_of(const SortArgs &a, int p) {
@@ -133,7 +135,10 @@ __global__ __launch_bounds__(kSortWaves * 64) void sort_kernel(SortArgs a) {
 // ---- dispatch --------------------------------------------------------------
 // y[place[t, j]] = x[t], in bytes: a workgroup takes 4 KB of a token's row,
 // reads them once and stores them top_k times, in unaligned accesses of 16
-// bytes if need be.  Bound by the stores.
+// bytes if need be, past the caches where rows are aligned (8191 x 8 rows of
+// 4096 bytes, half of them another rank's, with block scales: 31 us, 174 MB,
+// 5.6 TB/s; through the caches 45).  Taken by token and not by sorted row, a
+// row is read once however many experts it goes to.
 // Shorter rows share a workgroup, 2^shift threads each.
 constexpr int kPiece = 4096;
 template <bool SHORT>
@@ -195,7 +200,9 @@ int threads_shift(int64_t threads) {
 // ---- combine ---------------------------------------------------------------
 // d[t] = sum_j weight[t, j] y[place[t, j]] + residual[t]: a thread has eight
 // columns of a token and asks for up to eight rows before it adds the first.
-// Short rows share a workgroup as in the dispatch.
+// Short rows share a workgroup as in the dispatch.  Bound by memory (4099 x 8
+// rows of 4096 bf16 and a residual: 61 us, 336 MB, 5.5 TB/s; a single token's
+// 8 rows 3.9 us, a launch and two dependent loads).
 // Sums are in f32, in the order of j, rounded once.
 constexpr int kAtOnce = 8;
 
@@ -214,7 +221,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int shift) 
   float sum[8], add[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = add[i] = 0.f;
-  if (a.residual) get<E, 8>(a.residual, token * a.ldr + c, left, vec, add);
+  if (a.residual) get_once<E>(a.residual, token * a.ldr + c, left, vec, add);
   for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
     float v[kAtOnce][8], w[kAtOnce];
     int p[kAtOnce];
@@ -227,7 +234,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int shift) 
     for (int j = 0; j < kAtOnce; ++j) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-      if ((uint32_t)p[j] < (uint32_t)a.pairs) get<E, 8>(a.y, p[j] * a.ldy + c, left, vec, v[j]);
+      if ((uint32_t)p[j] < (uint32_t)a.pairs) get_once<E>(a.y, p[j] * a.ldy + c, left, vec, v[j]);
     }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
@@ -243,6 +250,9 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int shift) 
 
 // dy[place[t, j]] = weight[t, j] dd[t], dweight[t, j] = <dd[t], y[place[t, j]]>:
 // T threads a token, which go through its columns once for every AT choices.
+// With 8 elements a thread all loads of a token are in flight before the first
+// is used: 8192 x 4 rows of 4096 bf16 take 124 us (604 MB, 4.9 TB/s), with half
+// as many threads, twice around, and registers for 8 choices 159.
 template <class E, int T, int AT>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void combine_grad_kernel(CombineArgs a) {
   __shared__ float part[T == 64 ? 1 : AT][T / 64];
@@ -268,7 +278,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void combine_grad_kernel(Combine
       get<E, 8>(a.dd, token * a.ldd + c, left, vec, g);
 #pragma unroll
       for (int j = 0; j < AT; ++j)
-        if ((uint32_t)p[j] < (uint32_t)a.pairs) get<E, 8>(a.y, p[j] * a.ldy + c, left, vec, v[j]);
+        if ((uint32_t)p[j] < (uint32_t)a.pairs) get_once<E>(a.y, p[j] * a.ldy + c, left, vec, v[j]);
 #pragma unroll
       for (int j = 0; j < AT; ++j) {
         if ((uint32_t)p[j] >= (uint32_t)a.pairs) continue;

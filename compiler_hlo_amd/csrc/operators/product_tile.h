@@ -175,7 +175,10 @@ __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &t
 // e4m3 187 us, 2.9 PFLOP/s; 8191 x 22528 x 4096 gated bf16 with both halves
 // kept 1092 us.  The matrix cores are busy 74 - 81% of the cycles and the
 // power limit holds the clock at 1.6 - 1.9 GHz; a tile's end (sums out, the
-// next tile's first loads in) is 10 us.
+// next tile's first loads in) is 10 us.  With block scales 4096 x 4096 x 16384
+// e4m3 takes 225 us, 2.4 PFLOP/s: the vector unit's additions of the blocks'
+// sums share the issue with the matrix cores, which are busy 60% of the cycles
+// at 1.95 GHz.
 template <int HM, int HN>
 struct Shape {
   static constexpr int kWaves = 2 * (HN / 32), kThreads = kWaves * 64;
@@ -674,12 +677,23 @@ __device__ __forceinline__ bool expert_tile(const int32_t *offsets, int experts,
     }
     return (int)min((int64_t)((hi - lo + size - 1) / size) * per, (int64_t)kMost);
   };
-  int lo, hi;
-  int64_t all = 0;
-  for (int e = l; e - l < experts; e += 64) all += tiles(e, lo, hi);
+  auto scan = [&](int n) {  // the sum of the lanes up to this one
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) all += __shfl_xor(all, d);
-  const int total = __builtin_amdgcn_readfirstlane((int)min(all, (int64_t)0x7fffffff));
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(n, d);
+      n += l >= d ? o : 0;
+    }
+    return n;
+  };
+  // the first 64 experts' counts stay for the search
+  int lo, hi;
+  int n = tiles(l, lo, hi), sum = scan(n);
+  int64_t all = __builtin_amdgcn_readlane(sum, 63);
+  for (int first = 64; first < experts; first += 64) {
+    int a, b;
+    all += __builtin_amdgcn_readlane(scan(tiles(first + l, a, b)), 63);
+  }
+  const int total = (int)min(all, (int64_t)0x7fffffff);
   const int cut = CUT && total % 256 <= 128 ? total % 256 : 0, whole = total - cut;
   if (block >= whole + 2 * cut) return false;
   int id;
@@ -692,13 +706,7 @@ __device__ __forceinline__ bool expert_tile(const int32_t *offsets, int experts,
     id = whole + id / 2;
   }
   for (int first = 0; first < experts; first += 64) {
-    const int n = tiles(first + l, lo, hi);
-    int sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(sum, d);
-      sum += l >= d ? o : 0;
-    }
+    if (first > 0) n = tiles(first + l, lo, hi), sum = scan(n);
     const uint64_t hit = __ballot(id < sum);
     if (hit) {
       const int at = __builtin_ctzll(hit);

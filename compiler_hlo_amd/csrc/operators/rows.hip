@@ -675,7 +675,7 @@ __device__ __forceinline__ uint32_t sixteen_max(uint32_t v) {
 // each, so its largest magnitude takes four rotations within them.  A workgroup
 // has 16 blocks at a time, 2^shift of a row and as many rows as that leaves, R
 // times over; its scales go out through LDS, the rows of a block side by side.
-// Bound by memory (8191 x 11264 bf16 61 us, 280 MB, 4.6 TB/s; a row of 11264
+// Bound by memory (8191 x 11264 bf16 59 us, 280 MB, 4.7 TB/s; a row of 11264
 // 3.7 us, a launch and one pass of latency).
 template <class E, int R>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a, int shift) {
@@ -699,7 +699,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a, int shift
       const int row = (r0 + r) * per + (g >> shift);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[r][i] = 0.f;
-      if (row < rows && left > 0) get<E, 8>(a.x, (row0 + row) * a.ldx + c, left, vec, v[r]);
+      if (row < rows && left > 0) get_once<E>(a.x, (row0 + row) * a.ldx + c, left, vec, v[r]);
     }
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) {
