@@ -44,7 +44,7 @@ def embed() -> str:
 # scratch array, the operators' kernels); compiled with hipcc for gfx950,
 # without packed FP32, one process a file.
 HIP_SOURCES = ["scratch.hip", "operators/rows.hip", "operators/experts.hip", "operators/product.hip",
-               "operators/product_experts.hip", "operators/skinny.hip"]
+               "operators/product_experts.hip", "operators/product_experts_grad.hip", "operators/skinny.hip"]
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

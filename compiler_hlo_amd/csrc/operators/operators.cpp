@@ -162,9 +162,10 @@ double expert_threads(const hf_operator &op) {
   const Product &p = op.p1, &q = op.p2;
   double n = 0;
   const int64_t rows = p.tile == 0 ? 256 : p.tile == 1 ? 128 : 64, cols = p.tile == 0 ? 256 : 128;
-  if (p.on) n += (double)expert_tiles(p.m, p.experts, rows, 1) * (double)cdiv(p.n, p.gated ? cols / 2 : cols) + 128;
-  // dealt out in whole turns of eight chunks, a 64th of the tiles each at most
-  if (q.on) n += 1.125 * (double)q.experts * (double)cdiv(q.m, rows) * (double)cdiv(q.n, cols) + 8;
+  if (p.on)
+    n += p.splits * ((double)expert_tiles(p.m, p.experts, rows, 1) * (double)cdiv(p.n, p.gated ? cols / 2 : cols) + 128);
+  // dealt out in whole turns of eight chunks, a 128th of the tiles each at most
+  if (q.on) n += q.splits * (1.125 * (double)q.experts * (double)cdiv(q.m, rows) * (double)cdiv(q.n, cols) + 8);
   return n * (p.tile == 1 ? 256 : 512);
 }
 
@@ -308,7 +309,29 @@ void choose_experts(const hf_operator &op, Product &p, bool wide) {
   const int64_t from = op.d.flags & HF_OPERATOR_BLOCK_SCALES ? 640 : 160;
   const bool large = !wide && rows >= from && p.m / 256 * cdiv(p.n, p.gated ? 128 : 256) >= 128;
   p.tile = rows <= 24 ? 2 : large ? 0 : 1;
-  p.per_split = (int)std::max<int64_t>(1, cdiv(p.k, 128 / op.buf[0].elem()));
+  // The contraction is shared where the tiles are few, by an account of the
+  // times as in choose_tiles and choose (a launch more to add the parts counts 4
+  // us), for as many tiles as experts with half a tile of rows past their last
+  // whole one: 1 row of 8 experts, 2048 x 4096 bf16 by 8 12 us, whole 19; 200 of
+  // 4, 512 x 4096 by 16 19 and 36; 1024 of 4, 1024 x 4096 by 3 24 and 37.  8-bit
+  // sums whose scales go by the expert's rows stay whole.
+  const int64_t steps = std::max<int64_t>(1, cdiv(p.k, 128 / op.buf[0].elem())), size = p.tile == 2 ? 64 : 128;
+  const int64_t across = cdiv(p.n, p.gated ? 64 : 128), some = std::min(op.experts, p.m);
+  const int64_t groups = std::max<int64_t>(some, p.m / size + some / 2) * across, slots = p.tile == 2 ? 256 : 512;
+  p.ldp = p.gated ? 2 * up(p.n, 8) : up(p.n, 8);
+  p.per_split = (int)steps;
+  const bool whole = p.tile == 0 || (is_eight(op.d.dtype) && !(op.d.flags & HF_OPERATOR_BLOCK_SCALES));
+  double best = 1e300;
+  for (int64_t s = 1; p.on && s <= 16 && (s == 1 || (!whole && groups * s <= slots && steps >= 2 * s)); ++s) {
+    const double stage = p.tile == 2 ? std::max(0.3, 0.00325 * (double)std::min<int64_t>(groups * s, 256))
+                                     : groups * s <= 256 ? 0.6 : 0.95;
+    double us = (double)cdiv(groups * s, slots) * ((double)cdiv(steps, s) * stage + 3.0);
+    if (s > 1) us += 4.0 + 8.0 * (double)(s * p.m * p.ldp) / 5e6;
+    if (us >= best) continue;
+    best = us;
+    p.per_split = (int)cdiv(steps, s);
+    p.splits = (int)cdiv(steps, p.per_split);
+  }
 }
 
 // A gradient by expert: large tiles where db has 128 or more (16 experts of 256
@@ -318,6 +341,36 @@ void choose_experts_gradient(const hf_operator &op, Product &p, Product &q) {
   q.on = q.m > 0 && q.n > 0;
   p.experts = q.experts = op.experts;
   p.tile = q.tile = op.experts * cdiv(q.m, 256) * cdiv(q.n, 256) >= 128 ? 0 : 1;
+  // Small tiles that leave most of the chip idle share the contractions, by the
+  // same account: da's over b's rows, db's over twice the rows that an expert
+  // has if all have as many (5549 rows of one expert, 128 x 896 bf16 21 us, whole
+  // 61; 12 of 2, 3712 x 320 17 and 36).
+  p.ldp = q.ldp = up(q.n, 8);
+  const int64_t steps_p = std::max<int64_t>(1, cdiv(p.k, 64)), some = std::max<int64_t>(1, std::min(op.experts, p.m));
+  const int64_t steps_q = std::max<int64_t>(1, cdiv(2 * p.m / some, 64)), across = cdiv(q.n, 128);
+  const int64_t groups_p = p.on ? std::max<int64_t>(some, p.m / 128 + some / 2) * across : 0;
+  const int64_t groups_q = q.on ? op.experts * cdiv(q.m, 128) * across : 0;
+  p.per_split = (int)steps_p;
+  double best = 1e300;
+  for (int64_t s = 1; s <= 16 && (s == 1 || (p.on && p.tile == 1 && steps_p >= 2 * s)); ++s)
+    for (int64_t t = 1; t <= 16 && (t == 1 || (q.on && p.tile == 1 && steps_q >= 2 * t)); ++t) {
+      const int64_t all = groups_p * s + groups_q * t;
+      if ((s > 1 || t > 1) && all > 512) continue;
+      const double stage = all <= 256 ? 0.6 : 0.95;
+      double us = (double)std::max(p.on ? cdiv(steps_p, s) : 0, q.on ? cdiv(steps_q, t) : 0) * stage;
+      if (s > 1) us += 4.0 + 8.0 * (double)(s * p.m * p.ldp) / 5e6;
+      if (t > 1) us += 4.0 + 8.0 * (double)(t * op.experts * q.m * q.ldp) / 5e6;
+      if (us >= best) continue;
+      best = us;
+      p.per_split = (int)cdiv(steps_p, s);
+      p.splits = (int)cdiv(steps_p, p.per_split);
+      q.splits = (int)t;
+    }
+}
+
+// The partial sums' place of products by expert.
+void place_expert_partials(hf_operator &op, Product &p, int64_t rows) {
+  if (p.on && p.splits > 1) p.partial_at = take(op, p.splits * rows * p.ldp * 4);
 }
 
 void plan_norm(hf_operator &op) {
@@ -413,6 +466,7 @@ void plan_product(hf_operator &op) {
   }
   if (op.experts) {
     choose_experts(op, p, d.dtype == HF_F8E4M3 && f8_wide(d.out_dtype, p.k));
+    place_expert_partials(op, p, p.m);
     return;
   }
   const double whole = choose(d, p, elem);
@@ -489,6 +543,8 @@ void plan_product_grad(hf_operator &op) {
   q.b = a;
   if (op.experts) {
     choose_experts_gradient(op, p, q);
+    place_expert_partials(op, p, p.m);
+    place_expert_partials(op, q, op.experts * q.m);
     return;
   }
   choose_gradient(p, q);

@@ -153,8 +153,8 @@ struct ProductArgs {
   int32_t tiles_full;        // tiles 0 and 1: so many are one workgroup's, the others `splits` workgroups'
   int32_t splits, k_tiles_per_split;
   // splits > 1: [splits][shared tiles][part_rows][part_cols], the up half's
-  // columns after the gate's, or (strips, skinny) [splits][m][ldp]; s8: 32-bit
-  // integers
+  // columns after the gate's, or (strips, skinny, by expert) [splits][m][ldp]
+  // (db: [splits][experts * m][ldp]); s8: 32-bit integers
   float *partial;
   int32_t part_rows, part_cols;
   int64_t ldp;
@@ -168,12 +168,16 @@ struct ProductArgs {
   // b_expert bytes lie between two
   const int32_t *offsets;
   int32_t experts;
+  int32_t piece;             // in a workgroup: which of the splits
   int64_t b_expert;
   Epilogue e;
 };
 // What a launch of 256 or 512 threads a workgroup takes in tiles by expert.
 int64_t expert_tiles(int64_t m, int64_t experts, int64_t size, int64_t per);
 hipError_t launch_experts(const ProductArgs &a, hipStream_t s);
+// Adds the splits' sums of a.e.m rows (with offsets, of those that are an
+// expert's) and runs the epilogue.
+hipError_t launch_experts_fold(const ProductArgs &a, const int32_t *offsets, hipStream_t s);
 // The gradient by expert: da as above with b's rows as the contraction; db's
 // contraction runs over an expert's rows, its a_bytes and b_bytes are a row's,
 // its rows m and its results an expert's.

@@ -25,6 +25,7 @@ __global__ __launch_bounds__(HM == 128 ? 512 : 256, 2) void gradient_kernel(Prod
 template <class Step>
 __global__ __launch_bounds__(512, 2) void strip_kernel(ProductArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[Strip<Step>::kLds];
+  a.partial += (int64_t)blockIdx.y * a.m * a.ldp;
   strip_tile<Step>(a, (int)block_number<512>(blockIdx.x, blockIdx.z), blockIdx.y, blockIdx.x * 7u + blockIdx.y, lds);
 }
 

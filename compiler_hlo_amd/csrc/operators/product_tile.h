@@ -193,8 +193,12 @@ struct Shape {
 };
 
 // EXPERT: `a` is one expert's part of a product by experts, whose tiles are
-// numbered from 0 and are a workgroup's each.
-template <class Step, bool ACOL, bool BCOL, int HM, int HN, bool EXPERT = false>
+// numbered from 0 and are a workgroup's each (kWhole), or that of every one of
+// the splits (kSplit: piece a.piece, whose sums go to a.partial on).  They are
+// kernels of their own: with the choice made in one, small products of the
+// whole contraction take 1 us more.
+enum { kDense = 0, kWhole = 1, kSplit = 2 };
+template <class Step, bool ACOL, bool BCOL, int HM, int HN, int EXPERT = kDense>
 __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, char *lds) {
   typedef Shape<HM, HN> S;
   constexpr int WN = HN / 32, WAVES = S::kWaves, THREADS = S::kThreads, kStage = S::kStage, kPitch = S::kPitch;
@@ -220,7 +224,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
     const int xcd = id % 8, q = count / 8, r = count % 8;
     id = xcd * q + (xcd < r ? xcd : r) + id / 8;
   }
-  const int piece = part ? id / rest : 0, local = part ? id % rest : 0;
+  const int piece = EXPERT == kSplit ? a.piece : part ? id / rest : 0, local = part ? id % rest : 0;
   int tm, tn;
   tile_at(part ? a.tiles_full + local : id, tiles_m, tiles_n, tm, tn);
   const int m0 = tm * 2 * HM, n0 = tn * tile_n;
@@ -229,7 +233,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   constexpr int kStep = 128 / Step::kBytes;  // elements of the contraction a stage
   const int all = (a.k + kStep - 1) / kStep;
   const int k0 = piece * a.k_tiles_per_split;
-  const int kn = !part || all - k0 < a.k_tiles_per_split ? all - k0 : a.k_tiles_per_split;
+  const int kn = !(EXPERT == kSplit || part) || all - k0 < a.k_tiles_per_split ? all - k0 : a.k_tiles_per_split;
 
   // the operands' first bytes for this tile and what is left of them
   const int64_t a0 = ACOL ? (int64_t)m0 * Step::kBytes + (int64_t)k0 * kStep * a.lda
@@ -471,7 +475,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
   // consecutive columns of a row and a row's stores are contiguous.  A lane's
   // four sums are 16 bytes; the pad keeps neighbouring rows in different banks.
   const int l = threadIdx.x % 64;
-  const bool shared = part && a.splits > 1;
+  const bool shared = EXPERT == kSplit || (part && a.splits > 1);
   float *out = (float *)lds;
   const int shift = __builtin_ctz(tile_n / 8), per = 1 << shift;  // threads a row
 #pragma unroll
@@ -492,7 +496,13 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
       float v[8], u[8];
       load8<F32>(out + r * kPitch + c, v);
       if (gated) load8<F32>(out + r * kPitch + HN + c, u);
-      if (shared) {
+      if (EXPERT == kSplit) {
+        if (m < a.m && n < a.n) {
+          float *p = a.partial + m * a.ldp + n;
+          store8<F32>(p, v);
+          if (gated) store8<F32>(p + a.ldp / 2, u);
+        }
+      } else if (shared) {
         if (i * HM + r < a.part_rows && c < (gated ? a.part_cols / 2 : a.part_cols)) {
           float *p = a.partial + (((int64_t)piece * rest + local) * a.part_rows + i * HM + r) * a.part_cols + c;
           store8<F32>(p, v);
@@ -521,8 +531,8 @@ struct Strip {
   static constexpr int kLds = kStages * (kStage + kScale);
 };
 
-// Strip number `strip`, part number `piece` of the contraction; `seed` staggers
-// the workgroups.
+// Strip number `strip`, part number `piece` of the contraction, whose sums go to
+// a.partial on; `seed` staggers the workgroups.
 template <class Step>
 __device__ __forceinline__ void strip_tile(const ProductArgs &a, int strip, int piece, uint32_t seed, char *lds) {
   constexpr int HN = 64;
@@ -633,7 +643,7 @@ __device__ __forceinline__ void strip_tile(const ProductArgs &a, int strip, int 
     load8<F32>(out + m * kPitch + c, v);
     if (gated) load8<F32>(out + m * kPitch + HN + c, u);
     if (a.splits > 1) {
-      float *p = a.partial + ((int64_t)piece * a.m + m) * a.ldp + n;
+      float *p = a.partial + m * a.ldp + n;
       store8<F32>(p, v);
       if (gated) store8<F32>(p + a.ldp / 2, u);
     } else {
@@ -730,6 +740,7 @@ __device__ __forceinline__ ProductArgs part_of(const ProductArgs &a, int expert,
   p.a_bytes = a.a_bytes - row * a.lda;
   p.b = (const char *)a.b + expert * a.b_expert;
   p.m = p.e.m = rows;
+  p.partial = a.partial + ((int64_t)a.piece * a.m + row) * a.ldp;
   p.e.d = (char *)a.e.d + row * a.e.ldd * out;
   if (a.e.z) p.e.z = (char *)a.e.z + row * a.e.ldz * out;
   if (a.e.a_scale) p.e.a_scale = a.e.a_scale + row, p.e.b_scale = a.e.b_scale + expert * wide;
@@ -738,6 +749,20 @@ __device__ __forceinline__ ProductArgs part_of(const ProductArgs &a, int expert,
     p.b_scale = a.b_scale + expert * (int64_t)(a.e.gated ? 2 : 1) * a.b_scale_half * a.ldb_scale;
   }
   return p;
+}
+
+// A tile of 256 x 256 of an expert, or, where it has no more than 128 rows or
+// is cut, a half or two of them of 128 x 256, which take about 0.6 of its time.
+template <class Step, bool ACOL, bool BCOL>
+__device__ __forceinline__ void large_tile(const ProductArgs &a, const ExpertTile &t, int tiles_n, char *lds) {
+  int tm, tn;
+  tile_at(t.local, (t.rows + 255) / 256, tiles_n, tm, tn);
+  const int from = tm * 256 + (t.half > 0 ? 128 : 0), left = t.rows - from;
+  if (left <= 0) return;
+  if (t.half >= 0 || left <= 128)
+    product_tile<Step, ACOL, BCOL, 64, 128, kWhole>(part_of(a, t.expert, t.row + from, min(left, 128)), tn, lds);
+  else
+    product_tile<Step, ACOL, BCOL, 128, 128, kWhole>(part_of(a, t.expert, t.row, t.rows), t.local, lds);
 }
 
 }  // namespace hf

@@ -227,7 +227,27 @@ def test_workspaces():
 def test_tile_choices_by_expert(m, n, experts, dtype, want):
     kw = {"bf16": {}, "blocks": dict(dtype="f8e4m3", scales="blocks"), "f32": dict(dtype="f8e4m3", out_dtype="f32")}[dtype]
     p = H.Matmul(m, n, 2048, experts=experts, mode="plan", **kw).plan()
-    assert p["tile_rows"] == want and p["tile_cols"] == max(want, 128) and p["splits"] == 1
+    assert p["tile_rows"] == want and p["tile_cols"] == max(want, 128)
+
+
+@pytest.mark.parametrize("m, n, k, experts, dtype, splits", [
+    (1, 2048, 4096, 8, "bf16", 8),       # a token of 8 experts: 16 strips
+    (128, 1408, 4096, 32, "bf16", 1),    # strips enough
+    (200, 512, 4096, 4, "bf16", 16),
+    (200, 512, 4096, 4, "blocks", 11),
+    (200, 512, 4096, 4, "s8", 1),        # scales by the expert's rows: whole
+    (16384, 4096, 4096, 8, "bf16", 1),
+])
+def test_shared_contractions_by_expert(m, n, k, experts, dtype, splits):
+    kw = {"blocks": dict(dtype="f8e4m3", scales="blocks")}.get(dtype, dict(dtype=dtype))
+    p = H.Matmul(m, n, k, experts=experts, mode="plan", **kw).plan()
+    assert p["splits"] == splits and (p["workspace_bytes"] > 0) == (splits > 1)
+
+
+def test_shared_contractions_of_gradients_by_expert():
+    for m, n, k, experts, split in ((12, 3712, 320, 2, True), (5549, 128, 896, 1, True), (16384, 4096, 1408, 16, False),
+                                    (100, 512, 512, 8, False)):
+        assert (H.MatmulGrad(m, n, k, experts=experts, mode="plan").workspace_bytes > 0) == split
 
 
 @pytest.mark.parametrize("n, k, experts, want", [(4096, 1408, 16, 256), (512, 512, 8, 128), (1024, 1024, 8, 256)])

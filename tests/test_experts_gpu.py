@@ -508,6 +508,68 @@ def test_experts_large_tiles(dtype, counts):
         assert (d[z.shape[0]:] == 5.0).all() and (zs[z.shape[0]:] == 5.0).all()
 
 
+@pytest.mark.parametrize("dtype, out", [("bf16", "bf16"), ("f16", "f32"), ("blocks", "bf16"), ("blocks", "f32")])
+@pytest.mark.parametrize("counts, n, k", [([1, 0, 1, 0], 200, 4096), ([150, 0, 40, 10], 130, 4100), ([300, 0, 1, 129], 264, 2056),
+                                          ([0, 0, 3], 64, 8192)])
+def test_experts_shared_contraction(dtype, out, counts, n, k):
+    """Strips and small tiles whose contraction several workgroups share; the
+    fold leaves rows that are no expert's as they were."""
+    m, behind = sum(counts) + 4, 4
+    for parts in (1, 2):
+        g = gen(m + n + parts)
+        ops, z, mag = experts_operands(g, dtype, m, n, k, len(counts), parts, counts)
+        make = H.Matmul if parts == 1 else H.GatedFeedForward
+        op = make(m, n, k, "f8e4m3" if dtype == "blocks" else dtype, out_dtype=out, activation="relu", save=True,
+                  experts=len(counts), scales="blocks" if dtype == "blocks" else None)
+        assert op.plan()["splits"] > 1
+        say("experts shared", dtype, out, counts, n, k, parts, op.plan())
+        res = [b.empty("cuda") for b in op.results]
+        for t in res:
+            t.fill_(5.0)
+        d, zs = op(*ops, out=res)
+        live = m - behind
+        err = product_error(mag, k)
+        R.close(zs[:live], z, err, T[out])
+        want, off = R.act("relu", z[:, :n])[0], err[:, :n]
+        if parts == 2:
+            u = z[:, n:]
+            want, off = want * u, err[:, :n] * (u.abs() + err[:, n:]) + want.abs() * err[:, n:] + (want * u).abs() * 2.0 ** -24
+        R.close(d[:live], want, off, T[out])
+        assert (d[live:] == 5.0).all() and (zs[live:] == 5.0).all()
+        # offsets that begin past 0: rows before them too
+        if dtype == "bf16":
+            shifted = ops[-1] + 2
+            for t in res:
+                t.fill_(5.0)
+            op(*ops[:-1], shifted, out=res)
+            assert (res[0][:2] == 5.0).all() and (res[0][live + 2:] == 5.0).all() and not (res[0][2:live + 2] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts, n, k", [([1500], 128, 200), ([900, 0, 700], 96, 328), ([5, 0, 3], 2048, 136), ([0, 0], 64, 2000),
+                                          ([2000, 1], 130, 77)])
+def test_experts_gradient_shared_contraction(dtype, counts, n, k):
+    """da's contraction over many columns, db's over many rows, shared."""
+    experts, m, live = len(counts), sum(counts) + 3, sum(counts)
+    offsets = offsets_of(counts)
+    g = gen(m + n)
+    dd, a = normal(g, (m, n), dtype, 0.1), normal(g, (m, k), dtype)
+    b = normal(g, (experts * n, k), dtype, k ** -0.5)
+    for t in (dd, a):
+        t[live:] = float("nan")
+    op = H.MatmulGrad(m, n, k, dtype, experts=experts)
+    assert op.workspace_bytes > 0 or live == 0
+    say("experts gradient shared", dtype, counts, n, k, op.plan())
+    out = [x.empty("cuda") for x in op.results]
+    for t in out:
+        t.fill_(5.0)
+    da, db = op(dd, a, b, offsets.cuda(), out=out)
+    want = grads_want(R.f64(dd)[:live], R.f64(a)[:live], R.f64(b), offsets.tolist(), experts)
+    R.close(da[:live], want[0], R.sum_error(want[2], n), T[dtype])
+    R.close(db, want[1], R.sum_error(want[3], max(counts)), T[dtype])
+    assert (da[live:] == 5.0).all()
+
+
 def test_experts_large_tiles_all_cut():
     """128 large tiles, every one cut into two halves."""
     counts, n, k = [1024, 768, 256], 4096, 72
