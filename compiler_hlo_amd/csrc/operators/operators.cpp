@@ -979,7 +979,8 @@ hipError_t run_sort(const Call &c) {
 
 hipError_t run_dispatch(const Call &c) {
   const hf_operator &op = *c.op;
-  if (op.d.m == 0 || op.d.n == 0) return hipSuccess;
+  // rows of no columns still have their scale, where it is a row's
+  if (op.d.m == 0 || (op.d.n == 0 && op.i_a_scale < 0)) return hipSuccess;
   DispatchArgs a{};
   const int y = op.n_params;
   const int64_t elem = op.buf[0].elem();
