@@ -245,16 +245,20 @@ struct StepF8Block {
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }
   static __device__ __forceinline__ f32x4 bits(Acc c) { return c; }
 };
-// The same through f16 (see StepF8Wide); scales from the left.
+// The same through f16 (see StepF8Wide): the sum times b's power of two, which is
+// exact, is added with a's scale times b's mantissa, 0.5 .. 1, as the factor.
 struct StepF8BlockWide {
   typedef f32x4 Acc;
   static constexpr bool kBlock = true;
   static constexpr bool kWide = true;
   static constexpr int kBytes = 1;
   struct Scale {
-    float a, b;
+    float m, power;
   };
-  static __device__ __forceinline__ Scale scale(float a, float b) { return Scale{a, b}; }
+  static __device__ __forceinline__ Scale scale(float a, float b) {
+    const int e = min(max(__builtin_amdgcn_frexp_expf(b), -64), 64);
+    return Scale{a * __builtin_ldexpf(b, -e), __builtin_ldexpf(1.f, e)};
+  }
   static __device__ __forceinline__ f32x4 block(const i32x4 (&a)[2], const i32x4 (&b)[2], Scale) {
     f32x4 t = {0, 0, 0, 0};
 #pragma unroll
@@ -263,7 +267,7 @@ struct StepF8BlockWide {
   }
   static __device__ __forceinline__ Acc add(Acc c, f32x4 t, Scale s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i] * s.a, s.b, c[i]);
+    for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(t[i] * s.power, s.m, c[i]);
     return c;
   }
   static __device__ __forceinline__ f32x4 sums(Acc c) { return c; }

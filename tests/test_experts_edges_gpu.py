@@ -6,6 +6,7 @@ import torch
 import compiler_hlo_amd as H
 import experts_reference as X
 import operators_reference as R
+import operators_reference as R
 from test_operators_gpu import T, gen, say
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +33,51 @@ def test_dispatch_of_no_columns_in_blocks_writes_nothing():
         torch.empty((4, 0), dtype=T["f8e4m3"], device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda"),
         torch.empty((0, 4), device="cuda"))
     assert y.shape == (8, 0) and s.shape == (0, 8)
+
+
+# --------------------------------------------------------------------------
+# scales at the ends of f32
+# --------------------------------------------------------------------------
+# a row's scale, a weight's: their product is in f32's range, the sum times one
+# of them may not be
+FAR = [(1e36, 1e-36), (1e-36, 1e36), (1.9 * 2.0 ** 127, 1.9 * 2.0 ** -63), (1.9 * 2.0 ** -63, 1.9 * 2.0 ** 127),
+       (2.0 ** 127, 2.0 ** -127), (2.0 ** 90, 2.0 ** -140), (-1e36, 3e-37)]
+
+
+def far_product(m, n, k, out, sa, sb, experts, gated=False):
+    """(got, want, bound): rows of both signs whose sums reach 2^25 and 0."""
+    g = gen(m + n + k)
+    parts = 2 if gated else 1
+    a = torch.randint(-448, 449, (m, k), generator=g).float().to(T["f8e4m3"])
+    b = torch.randint(-448, 449, (parts * n, k), generator=g).float().to(T["f8e4m3"])
+    a[m - 1] = 0
+    av, bv = R.f64(a) * float(torch.tensor(sa).double()), R.f64(b) * float(torch.tensor(sb).double())
+    z, mag = av @ bv.T, av.abs() @ bv.abs().T
+    high, wide = -(-n // 128), -(-k // 128)
+    params = [a.cuda(), b.cuda(), torch.full((wide, m), sa, device="cuda"), torch.full((parts * high, wide), sb, device="cuda")]
+    more = {}
+    if experts:  # two experts of the same weight
+        params = [params[0], params[1].repeat(2, 1), params[2], params[3].repeat(2, 1),
+                  torch.tensor([0, m // 3, m], dtype=torch.int32, device="cuda")]
+        more = dict(experts=2)
+    if gated:
+        return H.GatedFeedForward(m, n, k, "f8e4m3", scales="blocks", out_dtype=out, activation="relu", save=True, **more)(*params)[1], z, mag
+    return H.Matmul(m, n, k, "f8e4m3", scales="blocks", out_dtype=out, **more)(*params), z, mag
+
+
+def far_error(mag, k):
+    """k products added in 32 bits, then a block's two roundings (scales'
+    product, addition) and those of the parts' additions."""
+    return R.sum_error(mag, k) + 8 * 2.0 ** -24 * mag
+
+
+@pytest.mark.parametrize("m, n", [(5, 48), (40, 200), (300, 300)])  # skinny, strips, tiles
+@pytest.mark.parametrize("k, out", [(128, "f32"), (100, "bf16"), (520, "f32")])
+def test_block_scales_far_apart_through_f16(m, n, k, out):
+    """f32 results and contractions of one block."""
+    for sa, sb in FAR + [(1.75 * 2.0 ** 60, 3 * 2.0 ** -149)]:
+        for experts in (False, True):
+            for gated in (False, True):
+                say("far scales through f16", m, n, k, out, sa, sb, experts, gated)
+                got, z, mag = far_product(m, n, k, out, sa, sb, experts, gated)
+                R.close(got, z, far_error(mag, k), T[out])
