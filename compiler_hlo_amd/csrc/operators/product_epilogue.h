@@ -215,10 +215,15 @@ struct StepS8 {
 // two scales: four multiply-adds a lane beside an instruction of 32 cycles.
 // The product of the two scales might leave f32's range where the sums are in
 // it, and two factors would cost four more operations.  So b's scale is taken
-// as m 2^e with e within +-64, where a block's sum times 2^e (the matrix
-// instruction's own block scale, e8m0) is in range, and a's scale times m is
-// the factor: m is in [1, 2), and beyond e's bounds it goes on towards b's
-// scale, so that the factor leaves the range only where the sum does.
+// as m 2^e with e within +-64, where a block's sum (0 or of magnitude 2^-18 ..
+// 2^25) times 2^e (the matrix instruction's own block scale, e8m0) is in range,
+// and a's scale times m is the factor.  m is in [0.5, 1), so no finite a takes
+// the factor out of range; beyond e's bounds m goes on towards b's scale, and the
+// factor overflows only where the scales' product passes 2^192, as every sum but
+// 0 does then.  Below 2^-125 an a times m is a denormal, rounded to a multiple of
+// 2^-149: an a of a few such units is off by up to a half of one.  (A power of
+// two for a's scale too would cost three more operations a factor, which stand
+// beside the matrix instructions, for scales of rows below 1e-35.)
 struct StepF8Block {
   typedef f32x4 Acc;
   static constexpr bool kBlock = true;
@@ -229,7 +234,7 @@ struct StepF8Block {
     int e;
   };
   static __device__ __forceinline__ Scale scale(float a, float b) {
-    const int e = min(max(__builtin_amdgcn_frexp_expf(b) - 1, -64), 64);
+    const int e = min(max(__builtin_amdgcn_frexp_expf(b), -64), 64);
     return Scale{a * __builtin_ldexpf(b, -e), e + 127};
   }
   static __device__ __forceinline__ f32x4 block(const i32x4 (&a)[2], const i32x4 (&b)[2], Scale s) {

@@ -81,3 +81,21 @@ def test_block_scales_far_apart_through_f16(m, n, k, out):
                 say("far scales through f16", m, n, k, out, sa, sb, experts, gated)
                 got, z, mag = far_product(m, n, k, out, sa, sb, experts, gated)
                 R.close(got, z, far_error(mag, k), T[out])
+
+
+@pytest.mark.parametrize("m, n", [(5, 48), (40, 200), (300, 300), (2100, 4100)])
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+def test_block_scales_far_apart_in_16_bits(m, n, out):
+    """The matrix instruction's own scale; 2100 x 4100 in the larger tiles."""
+    k, large = 520, m > 2000
+    assert (H.Matmul(m, n, k, "f8e4m3", scales="blocks", out_dtype=out, mode="plan").plan()["tile_rows"] == 256) == large
+    for sa, sb in FAR[:3] if large else FAR + [(1.75 * 2.0 ** 60, 3 * 2.0 ** -149)]:
+        if out == "f16":  # sums of 2^27 times the scales have to stay below 65504
+            if abs(sa * sb) > 2:
+                continue
+            sb = sb * 2.0 ** -20
+        for experts, gated in ((False, False), (True, False), (False, True))[:1 if large else 3]:
+            say("far scales", m, n, k, out, sa, sb, experts, gated)
+            got, z, mag = far_product(m, n, k, out, sa, sb, experts, gated)
+            # a block's sum is off by up to 2^-17 of its magnitudes
+            R.close(got, z, far_error(mag, k) + 2.0 ** -17 * mag, T[out])
