@@ -335,12 +335,17 @@ void choose_experts(const hf_operator &op, Product &p, bool wide) {
 }
 
 // A gradient by expert: large tiles where db has 128 or more (16 experts of 256
-// rows, 4096 x 1408 bf16 170 us, small 184; 8 of 64, 4096 x 4096 164 and 182).
+// rows, 4096 x 1408 bf16 170 us, small 184; 8 of 64, 4096 x 4096 164 and 182) that
+// hold no more than an eighth more sums than small ones, as every expert's weight
+// is rounded up to them (8192 rows of 128 experts, 128 x 128 17.2 us, small 11.8;
+// of 64, 384 x 384 37 and 26; 16384 of 60, 640 x 384 60 and 44; as many sums: 8192
+// of 200, 136 x 136 24.8 and 27.1).
 void choose_experts_gradient(const hf_operator &op, Product &p, Product &q) {
   p.on = p.m > 0 && p.n > 0;
   q.on = q.m > 0 && q.n > 0;
   p.experts = q.experts = op.experts;
-  p.tile = q.tile = op.experts * cdiv(q.m, 256) * cdiv(q.n, 256) >= 128 ? 0 : 1;
+  const int64_t large = op.experts * cdiv(q.m, 256) * cdiv(q.n, 256), small = op.experts * cdiv(q.m, 128) * cdiv(q.n, 128);
+  p.tile = q.tile = large >= 128 && large * 4 * 8 <= small * 9 ? 0 : 1;
   // Small tiles that leave most of the chip idle share the contractions, by the
   // same account: da's over b's rows, db's over twice the rows that an expert
   // has if all have as many (5549 rows of one expert, 128 x 896 bf16 21 us, whole

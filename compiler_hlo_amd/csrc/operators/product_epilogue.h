@@ -221,7 +221,7 @@ struct StepS8 {
 // the factor out of range; beyond e's bounds m goes on towards b's scale, and the
 // factor overflows only where the scales' product passes 2^192, as every sum but
 // 0 does then.  Below 2^-125 an a times m is a denormal, rounded to a multiple of
-// 2^-149: an a of a few such units is off by up to a half of one.  (A power of
+// 2^-149: an a of a few such units is off by up to one.  (A power of
 // two for a's scale too would cost three more operations a factor, which stand
 // beside the matrix instructions, for scales of rows below 1e-35.)
 struct StepF8Block {

@@ -516,7 +516,7 @@ typedef struct {
  *             f32 (gated: the gate's ceil(n / 128) rows, then the up half's; by
  *             expert: one such array after another)
  *   Scales of any size: the sum leaves f32's range only where the result does,
- *   but a row's scale below 2^-125 is taken to within 2^-150, and a block's sum
+ *   but a row's scale below 2^-125 is taken to within 2^-149, and a block's sum
  *   of 0 gives NaN where its scales' product is 2^192 or more in magnitude.
  *
  * place and offsets are read on the GPU.  Whatever they hold, no access leaves
