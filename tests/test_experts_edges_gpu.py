@@ -65,6 +65,12 @@ def far_product(m, n, k, out, sa, sb, experts, gated=False):
     return H.Matmul(m, n, k, "f8e4m3", scales="blocks", out_dtype=out, **more)(*params), z, mag
 
 
+# The 8-bit matrix instructions cut up to 7 of 8 consecutive products to multiples
+# of 2^-13 of the power of two of the largest one's factors, which is at most the
+# largest product: below 7 * 2^-13 of the sum of magnitudes.
+CUT = 7 * 2.0 ** -13
+
+
 def far_error(mag, k):
     """k products added in 32 bits, then a block's two roundings (scales'
     product, addition) and those of the parts' additions."""
@@ -97,5 +103,51 @@ def test_block_scales_far_apart_in_16_bits(m, n, out):
         for experts, gated in ((False, False), (True, False), (False, True))[:1 if large else 3]:
             say("far scales", m, n, k, out, sa, sb, experts, gated)
             got, z, mag = far_product(m, n, k, out, sa, sb, experts, gated)
-            # a block's sum is off by up to 2^-17 of its magnitudes
-            R.close(got, z, far_error(mag, k) + 2.0 ** -17 * mag, T[out])
+            R.close(got, z, far_error(mag, k) + CUT * mag, T[out])
+
+
+# --------------------------------------------------------------------------
+# sums of products of very different sizes
+# --------------------------------------------------------------------------
+# a last block of a few groups, and of more
+@pytest.mark.parametrize("m, n, k", [(m, n, k) for m, n in ((5, 48), (40, 200), (300, 300)) for k in (144, 160, 272, 1040)]
+                         + [(2100, 4100, 144), (2100, 4100, 520)])
+def test_sums_of_wide_spread_values(m, n, k):
+    """Values over the whole of e4m3 beside one another: f32 results are exact to
+    f32's rounding, 16-bit ones to the bound of the 8-bit instructions."""
+    g = gen(m + k)
+    spread = lambda r: (torch.exp(2.5 * torch.randn((r, k), generator=g)) * torch.randn((r, k), generator=g).sign()).clamp(-448, 448).to(T["f8e4m3"])  # noqa: E731
+    a, b = spread(m), spread(n)
+    high, wide = -(-n // 128), -(-k // 128)
+    for scales in ("rows", "blocks"):
+        if scales == "rows":
+            # f16's range holds the results
+            sa, sb = (torch.rand(m, generator=g) + 0.5) * 2.0 ** -12, torch.rand(n, generator=g) + 0.5
+            av, bv = R.f64(a) * R.f64(sa)[:, None], R.f64(b) * R.f64(sb)[:, None]
+        else:  # the last block, which is short, outweighs the others in some rows
+            sa, sb = torch.exp(torch.clamp(3 * torch.randn((wide, m), generator=g), max=7)) * 2.0 ** -24, torch.rand((high, wide), generator=g) + 0.5
+            av, bv = R.f64(a) * X.spread_rows(sa, k), R.f64(b) * X.spread_weight(sb, n, k)
+        z, mag = av @ bv.T, av.abs() @ bv.abs().T
+        for out in ("f32", "bf16", "f16"):
+            say("spread", m, n, k, scales, out)
+            params = [a.cuda(), b.cuda(), sa.cuda(), sb.cuda()]
+            err = far_error(mag, k) + (CUT * mag if out != "f32" else 0)
+            R.close(H.Matmul(m, n, k, "f8e4m3", scales=scales, out_dtype=out)(*params), z, err, T[out])
+            if m < 2000:
+                offsets = torch.tensor([0, m // 2, m], dtype=torch.int32, device="cuda")
+                two = [params[0], params[1].repeat(2, 1), params[2], sb.cuda().repeat(*([2] + [1] * (sb.dim() - 1)))]
+                R.close(H.Matmul(m, n, k, "f8e4m3", scales=scales, out_dtype=out, experts=2)(*two, offsets), z, err, T[out])
+
+
+def test_one_large_product_beside_small_ones():
+    """The bound's worst case: seven of eight products just below what is kept.
+    (f32 results have them all.)"""
+    k = 256
+    a, b = torch.zeros((1, k)), torch.ones((16, k))
+    a[0, :], a[0, ::8] = 7.5, 256
+    b[:, ::8] = 256
+    z = float((a.double() @ b[:1].double().T)[0, 0])
+    params = [a.to(T["f8e4m3"]).cuda(), b.to(T["f8e4m3"]).cuda(), torch.ones((2, 1), device="cuda"), torch.ones((1, 2), device="cuda")]
+    assert (H.Matmul(1, 16, k, "f8e4m3", scales="blocks", out_dtype="f32")(*params) == z).all()
+    got = H.Matmul(1, 16, k, "f8e4m3", scales="blocks")(*params)
+    assert ((got.double() - z).abs() <= z * (2.0 ** -8 + CUT)).all()
