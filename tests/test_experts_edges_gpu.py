@@ -7,7 +7,8 @@ import compiler_hlo_amd as H
 import experts_reference as X
 import operators_reference as R
 import operators_reference as R
-from test_operators_gpu import T, gen, say
+from test_experts_gpu import experts_operands, grads_want, offsets_of
+from test_operators_gpu import T, gen, normal, say
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +152,143 @@ def test_one_large_product_beside_small_ones():
     assert (H.Matmul(1, 16, k, "f8e4m3", scales="blocks", out_dtype="f32")(*params) == z).all()
     got = H.Matmul(1, 16, k, "f8e4m3", scales="blocks")(*params)
     assert ((got.double() - z).abs() <= z * (2.0 ** -8 + CUT)).all()
+
+
+# --------------------------------------------------------------------------
+# more than 64 experts in large tiles, shared contractions of both products of a
+# gradient, the library's own scratch memory
+# --------------------------------------------------------------------------
+MANY = [0 if e % 9 == 4 else 100 + (e * 37) % 190 for e in range(100)]
+
+
+def filled(op, value=5.0):
+    out = [b.empty("cuda") for b in op.results]
+    for t in out:
+        t.fill_(value)
+    return out
+
+
+@pytest.mark.parametrize("dtype, counts, n", [("bf16", MANY, 520), ("f16", MANY, 1000), ("s8", MANY, 520),
+                                              ("blocks", [v * 5 for v in MANY], 264)])
+def test_large_tiles_of_more_than_64_experts(dtype, counts, n):
+    """Experts past the first 64 are found by a second search; the last tiles are
+    whole or cut into halves."""
+    k, m, experts = 136, sum(counts) + 7, len(counts)
+    for parts in (1, 2):
+        g = gen(n + parts)
+        cols = n // parts
+        ops, z, mag = experts_operands(g, dtype, m, cols, k, experts, parts, counts)
+        make, half = H.Matmul if parts == 1 else H.GatedFeedForward, "f16" if dtype == "f16" else "bf16"
+        op = make(m, cols, k, "f8e4m3" if dtype == "blocks" else dtype, out_dtype=half, activation="relu", save=True,
+                  experts=experts, scales="blocks" if dtype == "blocks" else None)
+        assert op.plan()["tile_rows"] == 256
+        say("many experts", dtype, m, cols, k, parts, op.plan())
+        d, zs = op(*ops, out=filled(op))
+        live = z.shape[0]
+        R.close(zs[:live], z, far_error(mag, k) + (CUT * mag if dtype == "blocks" else 0), T[half])
+        assert (d[live:] == 5.0).all() and (zs[live:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("large", [True, False])
+def test_gradients_of_more_than_64_experts(dtype, large):
+    """db's tiles in the experts' own order."""
+    counts = MANY + [1, 0, 300]
+    experts, m, live, n, k = len(counts), sum(counts) + 5, sum(counts), 256, 512 if large else 640
+    offsets, g = offsets_of(counts), gen(k)
+    dd, a, b = normal(g, (m, n), dtype, 0.1), normal(g, (m, k), dtype), normal(g, (experts * n, k), dtype, k ** -0.5)
+    for t in (dd, a):
+        t[live:] = float("nan")
+    op = H.MatmulGrad(m, n, k, dtype, experts=experts)
+    assert op.plan()["tile_rows"] == (256 if large else 128)
+    say("gradient of many experts", dtype, op.plan())
+    da, db = op(dd, a, b, offsets.cuda(), out=filled(op))
+    want = grads_want(R.f64(dd)[:live], R.f64(a)[:live], R.f64(b), offsets.tolist(), experts)
+    R.close(da[:live], want[0], R.sum_error(want[2], n), T[dtype])
+    R.close(db, want[1], R.sum_error(want[3], max(counts)), T[dtype])
+    assert (da[live:] == 5.0).all()
+    for e in (e for e in range(experts) if counts[e] == 0):
+        assert (db[e * n:(e + 1) * n] == 0).all()
+
+
+def shares(op, m, n, k, experts):
+    """The parts of da's and of db's contraction.  Rows on 16 bytes and no
+    activation: the workspace holds nothing but their sums."""
+    plan = op.plan()
+    da = plan["splits"]
+    rest = plan["workspace_bytes"] - (-(-da * m * k * 4 // 256) * 256 if da > 1 else 0)
+    assert rest % (experts * n * k * 4) == 0
+    return da, max(1, rest // (experts * n * k * 4))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts, n, k", [([997], 2048, 128), ([1200, 0, 800], 2048, 64), ([1997, 3], 1536, 128),
+                                          ([697], 1032, 136)])
+def test_gradients_that_share_both_contractions(dtype, counts, n, k):
+    experts, m, live = len(counts), sum(counts) + 3, sum(counts)
+    offsets, g = offsets_of(counts), gen(m + n)
+    dd, a, b = normal(g, (m, n), dtype, 0.1), normal(g, (m, k), dtype), normal(g, (experts * n, k), dtype, k ** -0.5)
+    for t in (dd, a):
+        t[live:] = float("nan")
+    op = H.MatmulGrad(m, n, k, dtype, experts=experts)
+    assert min(shares(op, m, n, k, experts)) > 1, shares(op, m, n, k, experts)
+    say("both shared", dtype, counts, n, k, shares(op, m, n, k, experts))
+    da, db = op(dd, a, b, offsets.cuda(), out=filled(op))
+    want = grads_want(R.f64(dd)[:live], R.f64(a)[:live], R.f64(b), offsets.tolist(), experts)
+    R.close(da[:live], want[0], R.sum_error(want[2], n), T[dtype])
+    R.close(db, want[1], R.sum_error(want[3], max(counts)), T[dtype])
+    assert (da[live:] == 5.0).all()
+    # the library's scratch memory in the workspace's place
+    again = filled(op)
+    off = offsets.cuda()
+    op.launch_noalloc_ptrs([t.data_ptr() for t in (dd, a, b, off)], [t.data_ptr() for t in again],
+                           torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], da) and torch.equal(again[1], db)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "blocks"])
+@pytest.mark.parametrize("counts, n, k", [([1, 0, 1], 200, 4096), ([150, 0, 40], 136, 4096)])
+def test_shared_contractions_in_the_librarys_scratch_memory(dtype, counts, n, k):
+    m, g = sum(counts) + 2, gen(n)
+    ops, z, mag = experts_operands(g, dtype, m, n, k, len(counts), 1, counts)
+    op = H.Matmul(m, n, k, "f8e4m3" if dtype == "blocks" else dtype, experts=len(counts), scales="blocks" if dtype == "blocks" else None)
+    assert op.plan()["splits"] > 1
+    d, again = op(*ops, out=filled(op)), filled(op)[0]
+    op.launch_noalloc_ptrs([t.data_ptr() for t in ops], [again.data_ptr()], torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(d, again)
+    R.close(d[:z.shape[0]], z, far_error(mag, k) + (CUT * mag if dtype == "blocks" else 0), torch.bfloat16)
+
+
+def test_a_shared_gradient_under_replayed_graphs():
+    """Two captured gradients with a workspace each, replayed in turn with eager
+    work between, other rows and offsets at every replay."""
+    n, k, m = 2048, 128, 1000
+    g = gen(6)
+    sides = []
+    for _ in range(2):
+        op = H.MatmulGrad(m, n, k, experts=2)
+        p = [normal(g, (m, n), "bf16", 0.1), normal(g, (m, k), "bf16"), normal(g, (2 * n, k), "bf16", 0.1), offsets_of([500, 500]).cuda()]
+        launch = op.bind(*p)
+        launch()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            launch()
+        sides.append((op, p, launch.results, graph))
+    for turn in range(4):
+        for op, p, res, graph in sides:
+            p[0].copy_(torch.randn((m, n), generator=g))
+            first = [700, 0, 1000, 333][turn]
+            p[3].copy_(offsets_of([first, m - first]))
+            want = [t.clone() for t in op(*p)]
+            for t in res:
+                t.fill_(9.0)
+            torch.cuda.synchronize()
+            graph.replay()
+        torch.cuda.synchronize()
+        for op, p, res, graph in sides:
+            for t, w in zip(res, op(*p)):
+                assert torch.equal(t, w), turn
+        assert all(torch.isfinite(w.float()).all() for w in want)
