@@ -295,25 +295,25 @@ void place_partials(hf_operator &op, Product &p) {
 // kernel goes by the rows that an expert has if all have as many (measured with
 // the most liked of 8 to 64 experts at two to three times that):
 // - up to 24, strips (16 experts of 16 rows, gated 2048 x 4096 e4m3 with block
-//   scales 57 us, small tiles 68; 32 of 32 rows, 4096 x 1408 bf16 91 and 79);
-// - large tiles from 160 on (8 of 256, gated 4096 x 4096 bf16 177 us, small 203;
-//   32 of 96, gated 1408 x 4096 207 and 185), with block scales from 640 on, as
-//   two small ones a compute unit hide the scales' additions (8 of 512, gated
-//   4096 x 4096 235 us, small 221; of 1024 367 and 378), where they make 128 or
-//   more (8 of 256, 512 x 512 bf16 14.5 us, small 11.9);
+//   scales 59 us, small tiles 68; 32 of 32 rows, 4096 x 1408 bf16 87 and 76);
+// - large tiles from 160 on (8 of 256, gated 4096 x 4096 bf16 176 us, small 210;
+//   32 of 96, gated 1408 x 4096 201 and 177), with block scales from 192 on (32
+//   of 128, gated 1408 x 4096 120 us, small 107; of 256 135 and 165; 8 of 256,
+//   gated 4096 x 4096 113 and 126; of 1024 296 and 358), where they make 128 or
+//   more (8 of 256, 512 x 512 bf16 13.8 us, small 11.6);
 // - small tiles between.
 void choose_experts(const hf_operator &op, Product &p, bool wide) {
   p.on = p.m > 0 && p.n > 0;
   p.experts = op.experts;
   const int64_t rows = p.m / std::max<int64_t>(1, std::min(op.experts, p.m));
-  const int64_t from = op.d.flags & HF_OPERATOR_BLOCK_SCALES ? 640 : 160;
+  const int64_t from = op.d.flags & HF_OPERATOR_BLOCK_SCALES ? 192 : 160;
   const bool large = !wide && rows >= from && p.m / 256 * cdiv(p.n, p.gated ? 128 : 256) >= 128;
   p.tile = rows <= 24 ? 2 : large ? 0 : 1;
   // The contraction is shared where the tiles are few, by an account of the
   // times as in choose_tiles and choose (a launch more to add the parts counts 4
   // us), for as many tiles as experts with half a tile of rows past their last
   // whole one: 1 row of 8 experts, 2048 x 4096 bf16 by 8 12 us, whole 19; 200 of
-  // 4, 512 x 4096 by 16 19 and 36; 1024 of 4, 1024 x 4096 by 3 24 and 37.  8-bit
+  // 4, 512 x 4096 by 16 19 and 36; 1024 of 4, 1024 x 4096 by 3 25 and 37.  8-bit
   // sums whose scales go by the expert's rows stay whole.
   const int64_t steps = std::max<int64_t>(1, cdiv(p.k, 128 / op.buf[0].elem())), size = p.tile == 2 ? 64 : 128;
   const int64_t across = cdiv(p.n, p.gated ? 64 : 128), some = std::min(op.experts, p.m);
@@ -335,7 +335,7 @@ void choose_experts(const hf_operator &op, Product &p, bool wide) {
 }
 
 // A gradient by expert: large tiles where db has 128 or more (16 experts of 256
-// rows, 4096 x 1408 bf16 170 us, small 184; 8 of 64, 4096 x 4096 164 and 182) that
+// rows, 4096 x 1408 bf16 173 us, small 189; 8 of 64, 4096 x 4096 168 and 191) that
 // hold no more than an eighth more sums than small ones, as every expert's weight
 // is rounded up to them (8192 rows of 128 experts, 128 x 128 17.2 us, small 11.8;
 // of 64, 384 x 384 37 and 26; 16384 of 60, 640 x 384 60 and 44; as many sums: 8192

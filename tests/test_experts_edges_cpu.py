@@ -23,3 +23,16 @@ def test_a_gradients_tiles_are_not_mostly_padding(m, n, k, experts, want):
     assert H.MatmulGrad(m, n, k, experts=experts, mode="plan").plan()["tile_rows"] == want
     if n % 2 == 0:  # gated: 2n rows of db an expert
         assert H.GatedFeedForwardGrad(m, n // 2, k, experts=experts, mode="plan").plan()["tile_rows"] == want
+
+
+@pytest.mark.parametrize("rows, dtype, want", [
+    (159, "bf16", 128), (160, "bf16", 256),
+    (191, "blocks", 128), (192, "blocks", 256), (512, "blocks", 256),
+    (512, "f32", 128),   # block scales through f16 have no large tile
+])
+def test_the_rows_an_expert_from_which_tiles_are_large(rows, dtype, want):
+    kw = {"bf16": {}, "blocks": dict(dtype="f8e4m3", scales="blocks"),
+          "f32": dict(dtype="f8e4m3", scales="blocks", out_dtype="f32")}[dtype]
+    for experts, n in ((16, 4096), (40, 2048)):
+        assert H.Matmul(rows * experts, n, 2048, experts=experts, mode="plan", **kw).plan()["tile_rows"] == want
+        assert H.GatedFeedForward(rows * experts, n // 2, 2048, experts=experts, mode="plan", **kw).plan()["tile_rows"] == want

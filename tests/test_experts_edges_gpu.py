@@ -169,7 +169,7 @@ def filled(op, value=5.0):
 
 
 @pytest.mark.parametrize("dtype, counts, n", [("bf16", MANY, 520), ("f16", MANY, 1000), ("s8", MANY, 520),
-                                              ("blocks", [v * 5 for v in MANY], 264)])
+                                              ("blocks", [v * 5 for v in MANY], 264), ("blocks", [v + 60 for v in MANY], 520)])
 def test_large_tiles_of_more_than_64_experts(dtype, counts, n):
     """Experts past the first 64 are found by a second search; the last tiles are
     whole or cut into halves."""
