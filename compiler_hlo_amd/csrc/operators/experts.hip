@@ -17,7 +17,7 @@ namespace {
 // One workgroup does it all for up to 8192 pairs (192 pairs of 128 experts
 // 3.4 us, a launch and a few dependent steps); beyond that each chunk of pairs
 // has a workgroup, and a first launch counts by chunk (65528 pairs of 64
-// experts 4.6 + 6.3 us; every workgroup of the second adds up the counts of all
+// experts 4.6 + 6.2 us; every workgroup of the second adds up the counts of all
 // chunks by itself, which a third launch would cost more than).
 constexpr int kSortWaves = 16, kSortMost = 1024;  // waves; experts
 
@@ -251,8 +251,9 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int shift) 
 // dy[place[t, j]] = weight[t, j] dd[t], dweight[t, j] = <dd[t], y[place[t, j]]>:
 // T threads a token, which go through its columns once for every AT choices.
 // With 8 elements a thread all loads of a token are in flight before the first
-// is used: 8192 x 4 rows of 4096 bf16 take 124 us (604 MB, 4.9 TB/s), with half
-// as many threads, twice around, and registers for 8 choices 159.
+// is used: 8192 x 4 rows of 4096 bf16 take 119 us (604 MB, 5.1 TB/s); with half
+// as many threads, twice around, and registers for 8 choices 159 where this form
+// took 124, both through the caches.
 template <class E, int T, int AT>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void combine_grad_kernel(CombineArgs a) {
   __shared__ float part[T == 64 ? 1 : AT][T / 64];

@@ -9,8 +9,8 @@ namespace {
 // offsets on the GPU: the grid holds as many as any offsets can ask for, and a
 // workgroup without a tile ends at once.  Bound by the matrix cores and by what
 // the experts' ragged ends and the last round leave of the chip: 8198 rows of 8
-// experts, gated 4096 x 4096 bf16, 469 us, 1.17 PFLOP/s (up to 550 where the
-// last round has more than 128 tiles).
+// experts, gated 4096 x 4096 bf16, 462 us, 1.19 PFLOP/s, where the last round has
+// up to 128 tiles and is cut; 485 where it has 160, which are whole.
 template <class Step>
 __global__ __launch_bounds__(512, 2) void experts_large_kernel(ProductArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[Shape<128, 128>::lds(Step::kBlock)];

@@ -176,9 +176,10 @@ __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &t
 // kept 1092 us.  The matrix cores are busy 74 - 81% of the cycles and the
 // power limit holds the clock at 1.6 - 1.9 GHz; a tile's end (sums out, the
 // next tile's first loads in) is 10 us.  With block scales 4096 x 4096 x 16384
-// e4m3 takes 225 us, 2.4 PFLOP/s: the vector unit's additions of the blocks'
-// sums share the issue with the matrix cores, which are busy 60% of the cycles
-// at 1.95 GHz.
+// e4m3 takes 234 us, 2.35 PFLOP/s: a matrix instruction comes with 5.8 others of
+// the vector unit, 4 of them the additions of its block's sums and the rest
+// scales and addresses, and the matrix cores are busy 63% of the cycles at 1.92
+// GHz.
 template <int HM, int HN>
 struct Shape {
   static constexpr int kWaves = 2 * (HN / 32), kThreads = kWaves * 64;
