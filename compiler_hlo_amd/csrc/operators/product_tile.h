@@ -303,7 +303,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ch
     if (wave < WAVES / 2) {
       scale_from = (const char *)(a.a_scale + (int64_t)k0 * a.lda_scale + m0);
       scale_step = a.lda_scale * 4;
-      scale_bytes = (a.m - m0) * 4;
+      scale_bytes = min(a.m - m0, 2 * HM) * 4;  // the tile's rows: all those left may pass 2^31 bytes
     } else {
       const int half = (wave - WAVES / 2) / (WAVES / 4), n = gated ? n0 : n0 + half * HN;
       scale_from = (const char *)(a.b_scale + (min(n, a.n - 1) / 128 + (gated ? half * a.b_scale_half : 0)) * a.ldb_scale + k0);

@@ -292,3 +292,27 @@ def test_a_shared_gradient_under_replayed_graphs():
             for t, w in zip(res, op(*p)):
                 assert torch.equal(t, w), turn
         assert all(torch.isfinite(w.float()).all() for w in want)
+
+
+@pytest.mark.parametrize("by_expert", [False, True])
+def test_block_scales_of_more_than_2_29_rows(by_expert):
+    """Whole numbers, whose sums are exact; the scales of rows past 2^31 bytes."""
+    m, n, k = 2 ** 29 + 300, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = torch.empty((m, k), dtype=T["f8e4m3"], device="cuda")
+    scale = torch.empty((1, m), device="cuda")
+    for part, s in zip(a.split(1 << 24), scale[0].split(1 << 24)):
+        part.copy_(torch.randint(-3, 4, part.shape, generator=g, device="cuda", dtype=torch.int8))
+        s.copy_(torch.exp2(torch.randint(-2, 3, s.shape, generator=g, device="cuda").float()))
+    b = torch.randint(-3, 4, (n, k), generator=g, device="cuda").float()
+    sb = torch.full((1, 1), 2.0, device="cuda")
+    say("many rows", m, n, k, by_expert)
+    if by_expert:  # the second expert has all but the first ten rows
+        offsets = torch.tensor([0, 10, m], dtype=torch.int32, device="cuda")
+        op = H.Matmul(m, n, k, "f8e4m3", scales="blocks", experts=2)
+        d = op(a, b.repeat(2, 1).to(T["f8e4m3"]), scale, sb.repeat(2, 1), offsets)
+    else:
+        d = H.Matmul(m, n, k, "f8e4m3", scales="blocks")(a, b.to(T["f8e4m3"]), scale, sb)
+    for r in (0, 2 ** 28, 2 ** 29 - 500, m - 1000):
+        want = (a[r:r + 1000].float() @ b.T) * scale[0, r:r + 1000, None] * 2
+        assert torch.equal(d[r:r + 1000], want.to(torch.bfloat16)), r
